@@ -9,9 +9,18 @@ fails to load, importing this package raises.
     o, lse, mass = losa.dense_mass(q, k, v, L, block)        # construction step
     pat = losa.select(mass, block, tau=0.99)                   # frozen pattern
     o2, lse2 = losa.sparse_attn(q2, k2, v2, L, pat)            # every later step
+
+Training and the layout around it:
+
+    rope = losa.Rope((T, H, W), dims=(44, 42, 42))             # axes of the token grid
+    q, k, v = losa.rope_pack(xq, xk, xv, block, rope)          # [B, L, heads, d] -> packed
+    pat.prepare_backward()                                     # once per pattern
+    dq, dk, dv = losa.sparse_attn_bwd(q, k, v, o, lse, do, L, pat)
+    dxq, dxk, dxv = losa.rope_unpack(dq, dk, dv, L, rope)      # packed -> [B, L, heads, d]
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -30,6 +39,8 @@ STATUS = {0: "LOSA_OK", -1: "LOSA_ERR_ARG", -2: "LOSA_ERR_CUDA", -3: "LOSA_ERR_N
 EXPORTS = ("losa_dense_mass", "losa_select", "losa_dense_mass_select", "losa_pattern_info",
            "losa_pattern_export",
            "losa_pattern_import", "losa_select_noalloc", "losa_sparse_attn", "losa_free",
+           "losa_pattern_prepare_bwd", "losa_pattern_export_bwd", "losa_sparse_attn_bwd",
+           "losa_sparse_attn_bwd_workspace", "losa_rope_pack", "losa_rope_unpack",
            "losa_check_status", "losa_selftest_wait", "losa_set_wait_limit", "losa_exp2_eval",
            "losa_strerror", "losa_version")
 NOALLOC_MAX_ROWS = 65536  # LOSA_NOALLOC_MAX_ROWS
@@ -50,6 +61,12 @@ class PatternView(ctypes.Structure):
                 ("n_tiles", ctypes.c_int64), ("tile_entries", ctypes.c_int64),
                 ("tile_ptr", ctypes.c_void_p), ("tile_entry", ctypes.c_void_p),
                 ("tile_order", ctypes.c_void_p)]
+
+
+class RopeSpec(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int), ("grid", ctypes.c_int * 3), ("dim", ctypes.c_int * 3),
+                ("start", ctypes.c_int * 3), ("scale", ctypes.c_double * 3),
+                ("theta", ctypes.c_double), ("n_text", ctypes.c_int), ("pairing", ctypes.c_int)]
 
 
 def _load():
@@ -78,6 +95,22 @@ def _load():
     lib.losa_select_noalloc.restype = i32
     lib.losa_sparse_attn.argtypes = [vp, vp, vp, i32, i32, i32, f32, vp, vp, i32, vp, vp]
     lib.losa_sparse_attn.restype = i32
+    lib.losa_pattern_prepare_bwd.argtypes = [vp, vp]
+    lib.losa_pattern_prepare_bwd.restype = i32
+    lib.losa_pattern_export_bwd.argtypes = [vp, ctypes.POINTER(i64), vp, vp, vp, vp]
+    lib.losa_pattern_export_bwd.restype = i32
+    lib.losa_sparse_attn_bwd.argtypes = [vp, vp, vp, i32, vp, i32, vp, vp, i32, i32, i32, f32, vp,
+                                         vp, vp, vp, i32, vp, i64, vp]
+    lib.losa_sparse_attn_bwd.restype = i32
+    lib.losa_sparse_attn_bwd_workspace.argtypes = [vp, i32, i32, i32]
+    lib.losa_sparse_attn_bwd_workspace.restype = i64
+    spec = ctypes.POINTER(RopeSpec)
+    lib.losa_rope_pack.argtypes = [vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, spec, vp, vp, vp,
+                                   vp, i32, vp]
+    lib.losa_rope_pack.restype = i32
+    lib.losa_rope_unpack.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, i32, spec, vp, vp, vp,
+                                     vp, i32, vp, vp]
+    lib.losa_rope_unpack.restype = i32
     lib.losa_free.argtypes = [vp]
     lib.losa_free.restype = None
     lib.losa_check_status.argtypes = [vp]
@@ -181,6 +214,30 @@ class Pattern:
             self.close()
         except Exception:
             pass
+
+    def prepare_backward(self, stream=None):
+        """Builds the lists by key that sparse_attn_bwd walks: once, before
+        the first backward step and outside any capture."""
+        with torch.cuda.device(self.device):
+            _check("losa_pattern_prepare_bwd",
+                   _lib.losa_pattern_prepare_bwd(self.handle, _stream(stream)))
+        return self
+
+    def export_backward(self, stream=None):
+        """Host copies of the lists by key: key_ptr, key_entry, key_order."""
+        n = ctypes.c_int64()
+        with torch.cuda.device(self.device):
+            st = _lib.losa_pattern_export_bwd(self.handle, ctypes.byref(n), None, None, None,
+                                              _stream(stream))
+            _check("losa_pattern_export_bwd", st)
+            out = {k: torch.empty(m, dtype=torch.int32) for k, m in
+                   (("key_ptr", self.n_tiles + 1), ("key_entry", n.value),
+                    ("key_order", self.n_tiles))}
+            ptr = lambda t: t.data_ptr() if t.numel() else None
+            st = _lib.losa_pattern_export_bwd(self.handle, None, *(ptr(t) for t in out.values()),
+                                              _stream(stream))
+            _check("losa_pattern_export_bwd", st)
+        return out
 
     @property
     def rows(self):
@@ -288,6 +345,198 @@ def sparse_attn(q, k, v, L, pattern: Pattern, scale=None, out_dtype=torch.float3
                                _stream(stream))
     _check("losa_sparse_attn", st)
     return o, lse
+
+
+def _on(stream, device):
+    """The context of a call's own allocations: `device`, and `stream` if one
+    is given, so that a workspace freed on return is reused in that stream's
+    order."""
+    stack = contextlib.ExitStack()
+    stack.enter_context(torch.cuda.device(device))
+    if stream is not None:
+        stack.enter_context(torch.cuda.stream(stream))
+    return stack
+
+
+def sparse_attn_bwd(q, k, v, o, lse, do, L, pattern: Pattern, scale=None, out_dtype=None,
+                    dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Gradients (dq, dk, dv) of sparse_attn over the same pattern, which
+    pattern.prepare_backward() has been called on: o and lse are what the
+    forward call returned for q, k, v, do is the gradient of o. The results
+    have q's dtype unless out_dtype or the outputs say otherwise. Rows >= L of
+    the inputs are not used; those of the results are 0."""
+    _check_qkv(q, k, v)
+    B, H, Lp, d = q.shape
+    if (B, H, Lp) != (pattern.B, pattern.H, pattern.n_blocks * pattern.block):
+        raise ValueError("q/k/v shape does not match the pattern")
+    for name, t in (("o", o), ("do", do)):
+        if not (t.device == q.device and t.is_contiguous() and t.shape == q.shape):
+            raise ValueError(f"{name} must be a contiguous tensor of q's shape and device")
+    if not (lse.device == q.device and lse.is_contiguous() and lse.dtype == torch.float32
+            and lse.shape == q.shape[:3]):
+        raise ValueError("lse must be a contiguous fp32 tensor [B, H, L_pad] on q's device")
+    if not (q.device == k.device == v.device == torch.device(pattern.device)):
+        raise ValueError("q, k, v and the pattern must be on one device")
+    scale = default_scale(d) if scale is None else scale
+    given = [t for t in (dq, dk, dv) if t is not None]
+    if out_dtype is None:
+        out_dtype = given[0].dtype if given else q.dtype
+    for t in given:
+        if not (t.device == q.device and t.is_contiguous() and t.shape == q.shape
+                and t.dtype == out_dtype):
+            raise ValueError("dq, dk, dv must be contiguous tensors of q's shape and device "
+                             "and of one dtype")
+    with _on(stream, q.device):
+        dq, dk, dv = (torch.empty(q.shape, device=q.device, dtype=out_dtype) if t is None else t
+                      for t in (dq, dk, dv))
+        need = _lib.losa_sparse_attn_bwd_workspace(pattern.handle, _dtype_code(q),
+                                                   _dtype_code(do), d)
+        if need < 0:
+            _check("losa_sparse_attn_bwd_workspace", int(need))
+        if workspace is None:
+            workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+        elif not (workspace.device == q.device and workspace.is_contiguous()):
+            raise ValueError("workspace must be a contiguous tensor on q's device")
+        st = _lib.losa_sparse_attn_bwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), o.data_ptr(), _dtype_code(o),
+            lse.data_ptr(), do.data_ptr(), _dtype_code(do), d, int(L), float(scale),
+            pattern.handle, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _dtype_code(dq),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("losa_sparse_attn_bwd", st)
+    return dq, dk, dv
+
+
+class Rope:
+    """Rotary positions over the axes of a token grid.
+
+    grid    tokens along each axis, outermost first ((T, H, W) for video).
+    dims    features that each axis turns, from feature 0 on; those past
+            their sum are not turned.
+    theta   pair i of an axis with n features turns by position *
+            theta^(-2i/n).
+    start   position of each axis's first token (a later chunk's offset).
+    scale   factor on each axis's positions.
+    n_text  leading tokens that are not turned.
+    pairing "interleaved": features (2i, 2i + 1) of an axis turn together;
+            "halves": (i, i + n/2).
+    """
+
+    def __init__(self, grid, dims, theta=10000.0, start=None, scale=None, n_text=0,
+                 pairing="interleaved"):
+        n = len(dims)
+        start = (0,) * n if start is None else start
+        scale = (1.0,) * n if scale is None else scale
+        if not (1 <= n <= 3 and len(grid) == len(start) == len(scale) == n):
+            raise ValueError("grid, dims, start and scale must have 1 to 3 axes each")
+        if pairing not in ("interleaved", "halves"):
+            raise ValueError("pairing must be 'interleaved' or 'halves'")
+        if any(not -2**31 <= int(x) < 2**31 for x in (*grid, *dims, *start, n_text)):
+            raise ValueError("grid, dims, start and n_text must fit into 32 bits")
+        pad = lambda xs, fill: tuple(xs) + (fill,) * (3 - n)
+        self.n_axes = n
+        self.spec = RopeSpec(n, (ctypes.c_int * 3)(*map(int, pad(grid, 1))),
+                             (ctypes.c_int * 3)(*map(int, pad(dims, 0))),
+                             (ctypes.c_int * 3)(*map(int, pad(start, 0))),
+                             (ctypes.c_double * 3)(*map(float, pad(scale, 1.0))), float(theta),
+                             int(n_text), ("interleaved", "halves").index(pairing))
+
+
+def _check_positions(positions, B, L, rope, device):
+    if positions is None:
+        return None
+    if not (positions.device == device and positions.dtype == torch.int32
+            and positions.is_contiguous() and positions.shape == (B, L, rope.n_axes)):
+        raise ValueError("positions must be a contiguous int32 tensor [B, L, axes] on the "
+                         "inputs' device")
+    return positions.data_ptr()
+
+
+def _same(name, tensors, n_dims):
+    """The one device, shape and dtype of a call's tensors (None left out)."""
+    some = [t for t in tensors if t is not None]
+    if not some:
+        raise ValueError(f"one of {name} must be given")
+    for t in some:
+        if not (t.is_cuda and t.dim() == n_dims and t.shape == some[0].shape
+                and t.dtype == some[0].dtype and t.device == some[0].device):
+            raise ValueError(f"{name} must be CUDA tensors of one shape, dtype and device")
+    return some[0]
+
+
+def _token_strides(tensors):
+    flat = (ctypes.c_int64 * 9)()
+    for i, t in enumerate(tensors):
+        if t is None:
+            continue
+        if t.shape[3] > 1 and t.stride(3) != 1:
+            raise ValueError("features must be adjacent in memory (stride 1)")
+        flat[3 * i:3 * i + 3] = [t.stride(0), t.stride(1), t.stride(2)]
+    return flat
+
+
+_ptr = lambda t: None if t is None else t.data_ptr()
+
+
+def rope_pack(q, k, v, block, rope: Rope, positions=None, out_dtype=None, out=None, stream=None):
+    """Turns q and k [B, L, H, d] (any strides, features adjacent) by their
+    tokens' positions and lays q, k, v out as the attention calls take them:
+    [B, H, L_pad, d], L_pad the next multiple of `block`, padded rows 0. Any
+    of the three may be None. positions: int32 [B, L, axes] instead of the
+    rope's grid and start. out: the three tensors to write."""
+    x = _same("q, k, v", (q, k, v), 4)
+    B, L, H, d = x.shape
+    if block not in (32, 64, 128):
+        raise ValueError("block must be 32, 64 or 128")
+    Lp = (L + block - 1) // block * block
+    strides = _token_strides((q, k, v))
+    pos = _check_positions(positions, B, L, rope, x.device)
+    with _on(stream, x.device):
+        if out is None:
+            out = tuple(None if t is None else
+                        torch.empty(B, H, Lp, d, device=x.device, dtype=out_dtype or x.dtype)
+                        for t in (q, k, v))
+        y = _same("out", out, 4)
+        if any((a is None) != (b is None) for a, b in zip((q, k, v), out)):
+            raise ValueError("out must have a tensor for each of q, k, v that is given")
+        if y.device != x.device or y.shape != (B, H, Lp, d) or \
+                any(t is not None and not t.is_contiguous() for t in out) or \
+                (out_dtype is not None and y.dtype != out_dtype):
+            raise ValueError("out must be contiguous [B, H, L_pad, d] tensors on the inputs' "
+                             "device")
+        st = _lib.losa_rope_pack(_ptr(q), _ptr(k), _ptr(v), _dtype_code(x), strides, B, H, L, Lp,
+                                 d, ctypes.byref(rope.spec), pos, *map(_ptr, out), _dtype_code(y),
+                                 _stream(stream))
+    _check("losa_rope_pack", st)
+    return tuple(out)
+
+
+def rope_unpack(q, k, v, L, rope: Rope, positions=None, out_dtype=None, out=None, stream=None):
+    """The way back, and rope_pack's gradient: q, k, v [B, H, L_pad, d] to
+    [B, L, H, d], q and k turned by the negative angle. Any of the three may
+    be None (an attention output goes back as v alone). out: the tensors to
+    write, of any strides with adjacent features."""
+    x = _same("q, k, v", (q, k, v), 4)
+    B, H, Lp, d = x.shape
+    L = int(L)
+    if any(t is not None and not t.is_contiguous() for t in (q, k, v)):
+        raise ValueError("q, k, v must be contiguous [B, H, L_pad, d]")
+    pos = _check_positions(positions, B, L, rope, x.device)
+    with _on(stream, x.device):
+        if out is None:
+            out = tuple(None if t is None else
+                        torch.empty(B, L, H, d, device=x.device, dtype=out_dtype or x.dtype)
+                        for t in (q, k, v))
+        y = _same("out", out, 4)
+        if any((a is None) != (b is None) for a, b in zip((q, k, v), out)):
+            raise ValueError("out must have a tensor for each of q, k, v that is given")
+        if y.device != x.device or y.shape != (B, L, H, d) or \
+                (out_dtype is not None and y.dtype != out_dtype):
+            raise ValueError("out must be [B, L, H, d] tensors on the inputs' device")
+        st = _lib.losa_rope_unpack(_ptr(q), _ptr(k), _ptr(v), _dtype_code(x), B, H, L, Lp, d,
+                                   ctypes.byref(rope.spec), pos, *map(_ptr, out), _dtype_code(y),
+                                   _token_strides(out), _stream(stream))
+    _check("losa_rope_unpack", st)
+    return tuple(out)
 
 
 def exp2_eval(x, stream=None):

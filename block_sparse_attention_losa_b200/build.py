@@ -12,12 +12,15 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "liblosa.so")
-SOURCES = ["losa_api.cu", "losa_attention.cu", "losa_select.cu"]
+OBJ = os.path.join(HERE, "_build")
+SOURCES = ["losa_api.cu", "losa_attention.cu", "losa_select.cu", "losa_rope.cu",
+           "losa_backward.cu"]
 HEADERS = ["losa_device.cuh", "losa_attention.cuh", "losa_cut.cuh", "losa_internal.h"]
 
 
@@ -28,30 +31,54 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    deps.append(os.path.join(ROOT, "include", "losa.h"))
-    deps.append(os.path.abspath(__file__))
-    return any(os.path.getmtime(d) > t for d in deps)
+def _newer(path: str, deps) -> bool:
+    """Whether `path` exists and is newer than every dependency."""
+    return os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path)
+                                        for d in deps)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
-        return LIB
-    out_tmp = LIB + ".tmp"
+def _compile(src: str, force: bool) -> str:
+    """Compiles one source (unless its object is current) and returns the
+    object; the compiler's log is kept beside it."""
+    obj = os.path.join(OBJ, src.replace(".cu", ".o"))
+    deps = [os.path.join(CSRC, f) for f in [src] + HEADERS]
+    deps += [os.path.join(ROOT, "include", "losa.h"), os.path.abspath(__file__)]
+    if not force and _newer(obj, deps) and os.path.exists(obj + ".log"):
+        return obj
+    tmp = f"{obj}.{os.getpid()}.tmp"
     cmd = [nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3",
-           "-std=c++17", "-Xcompiler", "-fPIC", "-shared", "--expt-relaxed-constexpr",
-           "-Xptxas", "-v", "-I", os.path.join(ROOT, "include"), "-o", out_tmp]
-    cmd += [os.path.join(CSRC, f) for f in SOURCES]
+           "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr", "-Xptxas", "-v",
+           "-I", os.path.join(ROOT, "include"), "-c", "-o", tmp, os.path.join(CSRC, src)]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("nvcc failed:\n" + res.stdout + res.stderr)
+    with open(obj + ".log", "w") as f:
+        f.write(res.stderr)
+    os.replace(tmp, obj)
+    return obj
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
+    deps += [os.path.join(ROOT, "include", "losa.h"), os.path.abspath(__file__)]
+    if not force and _newer(LIB, deps):
+        return LIB
+    os.makedirs(OBJ, exist_ok=True)
+    with ThreadPoolExecutor(len(SOURCES)) as pool:
+        objects = list(pool.map(lambda src: _compile(src, force), SOURCES))
+    log = ""
+    for obj in objects:
+        with open(obj + ".log") as f:
+            log += f.read()
     if verbose:
-        sys.stderr.write(res.stderr)
-    check_attention_registers(res.stderr)
+        sys.stderr.write(log)
+    check_attention_registers(log)
+    out_tmp = LIB + ".tmp"
+    res = subprocess.run([nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared",
+                          "-Xcompiler", "-fPIC", "-o", out_tmp] + objects,
+                         capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("link failed:\n" + res.stdout + res.stderr)
     os.replace(out_tmp, LIB)
     return LIB
 

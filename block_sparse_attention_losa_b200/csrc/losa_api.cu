@@ -85,6 +85,50 @@ bool valid_attn_shape(int B, int H, int L, int L_pad, int d, int block) {
   return true;
 }
 
+// Checks what losa_rope_pack and losa_rope_unpack share. With `outputs` the
+// strides are those of tensors that are written: no two of their elements may
+// share a place.
+bool valid_rope(const void* const (&in)[3], void* const (&out)[3], int in_dtype, int out_dtype,
+                const int64_t* strides, bool outputs, int B, int H, int L, int L_pad, int d,
+                const losa_rope_spec* s, const int32_t* positions) {
+  if (!valid_dtype(in_dtype) || !valid_dtype(out_dtype) || !strides || !s) return false;
+  if (B < 1 || H < 1 || L < 1 || L_pad < L || L_pad - L >= 128) return false;
+  if ((d != 64 && d != 128) || int64_t(B) * H > 65535) return false;
+  if (!in[0] && !in[1] && !in[2]) return false;
+  const int in_size = in_dtype == LOSA_BF16 ? 2 : 4, out_size = out_dtype == LOSA_BF16 ? 2 : 4;
+  for (int t = 0; t < 3; ++t) {
+    if (!in[t] != !out[t]) return false;
+    if (!in[t]) continue;
+    if (reinterpret_cast<uintptr_t>(in[t]) % in_size || reinterpret_cast<uintptr_t>(out[t]) % out_size)
+      return false;
+    struct Dim {
+      int64_t stride, n;
+    } dims[3] = {{strides[3 * t], B}, {strides[3 * t + 1], L}, {strides[3 * t + 2], H}};
+    for (const Dim& x : dims)
+      if (x.stride < 0 || x.stride > (int64_t(1) << 40) / x.n) return false;
+    if (!outputs) continue;
+    std::sort(dims, dims + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+    int64_t reach = d;
+    for (const Dim& x : dims) {
+      if (x.n == 1) continue;
+      if (x.stride < reach) return false;
+      reach += x.stride * (x.n - 1);
+    }
+  }
+  if (s->n_axes < 1 || s->n_axes > 3 || s->n_text < 0 || s->n_text > L) return false;
+  if (s->pairing != LOSA_ROPE_INTERLEAVED && s->pairing != LOSA_ROPE_HALVES) return false;
+  if (!(std::isfinite(s->theta) && s->theta > 0.0)) return false;
+  int64_t features = 0, tokens = 1;
+  for (int a = 0; a < s->n_axes; ++a) {
+    if (s->dim[a] < 2 || s->dim[a] % 2 || s->dim[a] > d || !std::isfinite(s->scale[a])) return false;
+    features += s->dim[a];
+    if (s->grid[a] < 0) return false;
+    tokens = std::min<int64_t>(tokens * s->grid[a], int64_t(1) << 31);
+  }
+  if (features > d) return false;
+  return positions || tokens == L - s->n_text;
+}
+
 // Checks a host CSR for losa_pattern_import: row_ptr[0] = 0, every row
 // non-empty with at most n entries, columns strictly ascending in [0, n).
 // Returns the total of the 128-row tiles' union sizes, or -1 when invalid.
@@ -325,6 +369,118 @@ int losa_sparse_attn(const void* q, const void* k, const void* v, int in_dtype, 
   return LOSA_OK;
 }
 
+int losa_pattern_prepare_bwd(losa_pattern* p, void* stream) {
+  NvtxRange nvtx_range("losa_pattern_prepare_bwd");
+  if (!p) return LOSA_ERR_ARG;
+  if (p->key_mem) return LOSA_OK;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev != p->device) return LOSA_ERR_ARG;
+  return build_key_lists(p, static_cast<cudaStream_t>(stream));
+}
+
+int losa_pattern_export_bwd(const losa_pattern* p, int64_t* entries, int32_t* key_ptr,
+                            int32_t* key_entry, int32_t* key_order, void* stream) {
+  NvtxRange nvtx_range("losa_pattern_export_bwd");
+  if (!p || !p->key_mem) return LOSA_ERR_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (entries) *entries = p->key_entries;
+  struct Item {
+    void* dst;
+    const void* src;
+    size_t bytes;
+  } items[] = {{key_ptr, p->key_ptr, size_t(p->n_tiles + 1) * 4},
+               {key_entry, p->key_entry, size_t(p->key_entries) * 4},
+               {key_order, p->key_order, size_t(p->n_tiles) * 4}};
+  for (const Item& it : items)
+    if (it.dst && cudaMemcpyAsync(it.dst, it.src, it.bytes, cudaMemcpyDefault, s) != cudaSuccess)
+      return LOSA_ERR_CUDA;
+  return cudaStreamSynchronize(s) == cudaSuccess ? LOSA_OK : LOSA_ERR_CUDA;
+}
+
+int64_t losa_sparse_attn_bwd_workspace(const losa_pattern* p, int in_dtype, int do_dtype, int d) {
+  if (!p || !valid_dtype(in_dtype) || !valid_dtype(do_dtype) || (d != 64 && d != 128))
+    return LOSA_ERR_ARG;
+  return int64_t(backward_workspace(p, d, in_dtype == LOSA_BF16, do_dtype == LOSA_BF16));
+}
+
+int losa_sparse_attn_bwd(const void* q, const void* k, const void* v, int in_dtype, const void* o,
+                         int o_dtype, const float* lse, const void* d_o, int do_dtype, int d,
+                         int L, float scale, const losa_pattern* p, void* dq, void* dk, void* dv,
+                         int out_dtype, void* workspace, int64_t workspace_bytes, void* stream) {
+  NvtxRange nvtx_range("losa_sparse_attn_bwd");
+  if (!q || !k || !v || !o || !lse || !d_o || !p || !dq || !dk || !dv || !workspace)
+    return LOSA_ERR_ARG;
+  if (!valid_dtype(in_dtype) || !valid_dtype(o_dtype) || !valid_dtype(do_dtype) ||
+      !valid_dtype(out_dtype))
+    return LOSA_ERR_ARG;
+  const int L_pad = p->n_blocks * p->block;
+  if (!valid_attn_shape(p->B, p->H, L, L_pad, d, p->block) || !p->key_mem) return LOSA_ERR_ARG;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev != p->device) return LOSA_ERR_ARG;
+  if (!(std::isfinite(scale) && scale > 0.f)) return LOSA_ERR_ARG;
+  for (const void* x : {q, k, v, o, d_o, static_cast<const void*>(dq),
+                        static_cast<const void*>(dk), static_cast<const void*>(dv),
+                        static_cast<const void*>(workspace)})
+    if (!aligned16(x)) return LOSA_ERR_ARG;
+  if (workspace_bytes < losa_sparse_attn_bwd_workspace(p, in_dtype, do_dtype, d))
+    return LOSA_ERR_ARG;
+  if (!is_sm100()) return LOSA_ERR_UNSUPPORTED;
+  BackwardCall c{};
+  c.q = q;
+  c.k = k;
+  c.v = v;
+  c.in_bf16 = in_dtype == LOSA_BF16;
+  c.o = o;
+  c.o_bf16 = o_dtype == LOSA_BF16;
+  c.lse = lse;
+  c.d_o = d_o;
+  c.do_bf16 = do_dtype == LOSA_BF16;
+  c.d = d;
+  c.L = L;
+  c.scale = scale;
+  c.p = p;
+  c.dq = dq;
+  c.dk = dk;
+  c.dv = dv;
+  c.out_bf16 = out_dtype == LOSA_BF16;
+  c.workspace = workspace;
+  return launch_backward(c, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LOSA_OK
+                                                                             : LOSA_ERR_CUDA;
+}
+
+int losa_rope_pack(const void* q, const void* k, const void* v, int in_dtype,
+                   const int64_t* strides, int B, int H, int L, int L_pad, int d,
+                   const losa_rope_spec* spec, const int32_t* positions, void* q_out, void* k_out,
+                   void* v_out, int out_dtype, void* stream) {
+  NvtxRange nvtx_range("losa_rope_pack");
+  const void* const in[3] = {q, k, v};
+  void* const out[3] = {q_out, k_out, v_out};
+  if (!valid_rope(in, out, in_dtype, out_dtype, strides, false, B, H, L, L_pad, d, spec,
+                  positions))
+    return LOSA_ERR_ARG;
+  if (!is_sm100()) return LOSA_ERR_UNSUPPORTED;
+  const RopeCall c{{q, k, v},       {q_out, k_out, v_out},  strides, in_dtype == LOSA_BF16,
+                   out_dtype == LOSA_BF16, false, B, H, L, L_pad, d, spec, positions};
+  return launch_rope(c, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LOSA_OK
+                                                                         : LOSA_ERR_CUDA;
+}
+
+int losa_rope_unpack(const void* q, const void* k, const void* v, int in_dtype, int B, int H,
+                     int L, int L_pad, int d, const losa_rope_spec* spec,
+                     const int32_t* positions, void* q_out, void* k_out, void* v_out,
+                     int out_dtype, const int64_t* strides, void* stream) {
+  NvtxRange nvtx_range("losa_rope_unpack");
+  const void* const in[3] = {q, k, v};
+  void* const out[3] = {q_out, k_out, v_out};
+  if (!valid_rope(in, out, in_dtype, out_dtype, strides, true, B, H, L, L_pad, d, spec, positions))
+    return LOSA_ERR_ARG;
+  if (!is_sm100()) return LOSA_ERR_UNSUPPORTED;
+  const RopeCall c{{q, k, v},       {q_out, k_out, v_out}, strides, in_dtype == LOSA_BF16,
+                   out_dtype == LOSA_BF16, true, B, H, L, L_pad, d, spec, positions};
+  return launch_rope(c, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LOSA_OK
+                                                                         : LOSA_ERR_CUDA;
+}
+
 void losa_free(losa_pattern* p) {
   if (!p) return;
   NvtxRange nvtx_range("losa_free");
@@ -333,6 +489,7 @@ void losa_free(losa_pattern* p) {
   cudaSetDevice(p->device);
   if (p->fixed_mem) cudaFreeAsync(p->fixed_mem, p->stream);
   if (p->list_mem) cudaFreeAsync(p->list_mem, p->stream);
+  if (p->key_mem) cudaFreeAsync(p->key_mem, p->stream);
   cudaSetDevice(prev);
   delete p;
 }

@@ -25,6 +25,15 @@ struct losa_pattern {
   int32_t* tile_ptr;
   int32_t* tile_entry;
   int32_t* tile_order;
+  // The same pattern by key (losa_pattern_prepare_bwd; null before): 128-row
+  // key tiles with the union of the query blocks that keep one of their key
+  // blocks, entry = I | m << 16, bit c of m set when query block I keeps the
+  // tile's c-th key block.
+  void* key_mem;
+  int64_t key_entries;
+  int32_t* key_ptr;
+  int32_t* key_entry;
+  int32_t* key_order;
 };
 
 namespace losa {
@@ -131,5 +140,41 @@ void select_abort(SelectJob& job);
 int import_pattern(const int32_t* row_ptr, const int32_t* col_idx, const int64_t* retained_fx,
                    const int64_t* total_fx, int B, int H, int n, int block,
                    int64_t tile_entries, losa_pattern** out, cudaStream_t stream);
+
+// Builds the pattern's lists by key tile (losa_pattern_prepare_bwd) and
+// synchronises `stream`. Returns a losa_status.
+int build_key_lists(losa_pattern* p, cudaStream_t stream);
+
+// One call of losa_sparse_attn_bwd, validated by the caller.
+struct BackwardCall {
+  const void *q, *k, *v;
+  bool in_bf16;
+  const void* o;
+  bool o_bf16;
+  const float* lse;
+  const void* d_o;
+  bool do_bf16;
+  int d, L;
+  float scale;
+  const losa_pattern* p;
+  void *dq, *dk, *dv;
+  bool out_bf16;
+  void* workspace;
+};
+size_t backward_workspace(const losa_pattern* p, int d, bool in_bf16, bool do_bf16);
+cudaError_t launch_backward(const BackwardCall& c, cudaStream_t stream);
+
+// One call of losa_rope_pack (unpack false) or losa_rope_unpack, validated
+// by the caller; strides belong to the token-major side.
+struct RopeCall {
+  const void* in[3];
+  void* out[3];
+  const int64_t* strides;
+  bool in_bf16, out_bf16, unpack;
+  int B, H, L, L_pad, d;
+  const losa_rope_spec* spec;
+  const int32_t* positions;
+};
+cudaError_t launch_rope(const RopeCall& c, cudaStream_t stream);
 
 }  // namespace losa

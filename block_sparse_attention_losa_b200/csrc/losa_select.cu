@@ -369,6 +369,45 @@ __global__ void __launch_bounds__(kSelThreads)
   }
 }
 
+// Union entries of one 128-row key tile: the query blocks that keep one of
+// its key blocks. A thread looks the tile's first key block up in a query
+// block's ascending columns; the tile's other key blocks follow it there.
+// kWrite as in csr_tile_kernel.
+template <bool kWrite>
+__global__ void __launch_bounds__(kSelThreads)
+    key_tile_kernel(const int* __restrict__ row_ptr, const int* __restrict__ col_idx, int n,
+                    int bpt, int n_qt, int* __restrict__ tile_count,
+                    const int* __restrict__ tile_ptr, int* __restrict__ tile_entry) {
+  using Scan = cub::BlockScan<int, kSelThreads>;
+  __shared__ typename Scan::TempStorage tmp;
+  const int t = blockIdx.x;
+  const int bh = t / n_qt;
+  const int J0 = (t - bh * n_qt) * bpt;
+  int base = kWrite ? tile_ptr[t] : 0;
+  for (int c0 = 0; c0 < n; c0 += kSelThreads) {
+    const int I = c0 + threadIdx.x;
+    unsigned m = 0;
+    if (I < n) {
+      const int end = row_ptr[bh * n + I + 1];
+      int lo = row_ptr[bh * n + I], hi = end;
+      while (lo < hi) {  // first column >= J0
+        const int mid = (lo + hi) >> 1;
+        if (col_idx[mid] < J0)
+          lo = mid + 1;
+        else
+          hi = mid;
+      }
+      for (; lo < end && col_idx[lo] < J0 + bpt; ++lo) m |= 1u << (col_idx[lo] - J0);
+    }
+    int ex, tot;
+    Scan(tmp).ExclusiveSum(int(m != 0), ex, tot);
+    __syncthreads();
+    if (kWrite && m) tile_entry[base + ex] = I | int(m << 16);
+    base += tot;
+  }
+  if (!kWrite && threadIdx.x == 0) tile_count[t] = base;
+}
+
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
@@ -610,6 +649,59 @@ int import_pattern(const int32_t* row_ptr, const int32_t* col_idx, const int64_t
   p->fixed_mem = fixed;
   p->list_mem = lists;
   *out = p;
+  return LOSA_OK;
+}
+
+int build_key_lists(losa_pattern* p, cudaStream_t stream) {
+  const int BH = p->B * p->H, n = p->n_blocks;
+  const int bpt = 128 / p->block;
+  const int64_t T = p->n_tiles;
+  const int64_t n_keys = int64_t(BH) * (n + 1);
+  // Every entry holds at least one kept pair, so nnz bounds the list and its
+  // size need not be known before it is written.
+  const size_t o_ord = align256((T + 1) * 4);
+  const size_t o_ent = o_ord + align256(T * 4);
+  const size_t bytes = o_ent + align256(size_t(p->nnz) * 4);
+  const size_t s_hist = align256(T * 4);
+  const size_t s_cur = s_hist + align256(n_keys * 4);
+  const size_t scratch_bytes = s_cur + align256((n_keys + 1) * 4);
+  char* mem = static_cast<char*>(pool_alloc(bytes, stream));
+  char* scratch = static_cast<char*>(pool_alloc(scratch_bytes, stream));
+  auto fail = [&](int code) {
+    if (mem) cudaFreeAsync(mem, stream);
+    if (scratch) cudaFreeAsync(scratch, stream);
+    return code;
+  };
+  if (!mem || !scratch) return fail(LOSA_ERR_NOMEM);
+  auto* ptr = reinterpret_cast<int32_t*>(mem);
+  auto* order = reinterpret_cast<int32_t*>(mem + o_ord);
+  auto* entry = reinterpret_cast<int32_t*>(mem + o_ent);
+  auto* count = reinterpret_cast<int*>(scratch);
+  auto* hist = reinterpret_cast<int*>(scratch + s_hist);
+  auto* cursor = reinterpret_cast<int*>(scratch + s_cur);
+  key_tile_kernel<false><<<unsigned(T), kSelThreads, 0, stream>>>(
+      p->row_ptr, p->col_idx, n, bpt, p->n_qt, count, nullptr, nullptr);
+  scan_kernel<<<1, 1024, 0, stream>>>(count, int(T), ptr);
+  key_tile_kernel<true><<<unsigned(T), kSelThreads, 0, stream>>>(
+      p->row_ptr, p->col_idx, n, bpt, p->n_qt, nullptr, ptr, entry);
+  cudaMemsetAsync(hist, 0, n_keys * sizeof(int), stream);
+  const int og = int(std::min<int64_t>((T + 255) / 256, 1024));
+  order_hist_kernel<<<og, 256, 0, stream>>>(count, int(T), p->n_qt, n, hist);
+  scan_kernel<<<1, 1024, 0, stream>>>(hist, int(n_keys), cursor);
+  order_scatter_kernel<<<og, 256, 0, stream>>>(count, int(T), p->n_qt, n, cursor, order);
+  int total = 0;
+  if (cudaGetLastError() != cudaSuccess ||
+      cudaMemcpyAsync(&total, ptr + T, sizeof(int), cudaMemcpyDeviceToHost, stream) !=
+          cudaSuccess ||
+      cudaFreeAsync(scratch, stream) != cudaSuccess)
+    return fail(LOSA_ERR_CUDA);
+  scratch = nullptr;
+  if (cudaStreamSynchronize(stream) != cudaSuccess) return fail(LOSA_ERR_CUDA);
+  p->key_mem = mem;
+  p->key_entries = total;
+  p->key_ptr = ptr;
+  p->key_entry = entry;
+  p->key_order = order;
   return LOSA_OK;
 }
 

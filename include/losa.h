@@ -246,6 +246,135 @@ int losa_sparse_attn(const void* q, const void* k, const void* v, int in_dtype, 
                      int L, float scale, const losa_pattern* p,
                      void* o, int out_dtype, float* lse, void* stream);
 
+/*
+ * Training. losa_sparse_attn_bwd is the gradient of losa_sparse_attn over the
+ * same frozen pattern (and of losa_dense_mass's O with a pattern that keeps
+ * every block; the masses carry no gradient). It walks the pattern by query
+ * block and by key block, so losa_pattern_prepare_bwd has to be called once
+ * on a pattern before: it builds the lists by key, allocates them from the
+ * library's pool and synchronises `stream` once, so that they can then be
+ * used on any stream. A second call does nothing. Not for use while another
+ * thread uses the pattern, nor during stream capture.
+ *   Returns LOSA_ERR_ARG for a null pattern or a current device other than
+ *   the one the pattern was built on, LOSA_ERR_NOMEM, LOSA_ERR_CUDA.
+ */
+int losa_pattern_prepare_bwd(losa_pattern* p, void* stream);
+
+/*
+ * losa_pattern_export_bwd - copies the lists by key into caller buffers (host
+ * or device memory; NULL skips one) and synchronises `stream`: per 128-row
+ * key tile (b, h, t), key_entry[key_ptr[tile] .. key_ptr[tile + 1]) holds
+ * I | (m << 16), ascending query blocks I, bit c of m set when I keeps the
+ * tile's c-th key block; key_order [n_tiles] lists the tiles head by head,
+ * longest first. *entries (may be NULL) receives key_ptr[n_tiles].
+ *   Returns LOSA_ERR_ARG for a null pattern or one not prepared,
+ *   LOSA_ERR_CUDA.
+ */
+int losa_pattern_export_bwd(const losa_pattern* p, int64_t* entries, int32_t* key_ptr,
+                            int32_t* key_entry, int32_t* key_order, void* stream);
+
+/*
+ * losa_sparse_attn_bwd - gradients of losa_sparse_attn.
+ *
+ *   q, k, v   [B, H, L_pad, d] device, in_dtype: the forward call's inputs.
+ *   o, lse    what the forward call returned for them: O (o_dtype) and the
+ *             row log-sum-exp over the retained keys.
+ *   d_o       [B, H, L_pad, d], do_dtype: the gradient of O.
+ *   dq, dk, dv  [B, H, L_pad, d], out_dtype, written whole; rows >= L are 0.
+ *             With P_ij = exp(scale q_i.k_j - lse_i) on the kept pairs and
+ *             D_i = d_o_i . o_i:  dV = P^T dO, dS = P (dO V^T - D),
+ *             dQ = scale dS K, dK = scale dS^T Q. A key block that no query
+ *             block keeps gets 0.
+ *   workspace at least losa_sparse_attn_bwd_workspace(...) bytes of device
+ *             memory, 16-byte aligned, the call's own until it has run: calls
+ *             or captured graphs that may run at the same time need one each.
+ *   Rows >= L of every input are not used, whatever they hold. No output may
+ *   overlap an input, the workspace or another output.
+ *   bf16 q, k, v run on tensor cores: P and dS are rounded to bf16 as their
+ *   operands (half a unit in the 8th bit each), as is a fp32 d_o; all sums
+ *   are fp32. fp32 q, k, v run in fp32 throughout (no tf32 rounding). No
+ *   atomics: a call's results are the same bits every time.
+ *   Does not allocate or synchronise, so it can be captured in a CUDA graph.
+ *   Returns LOSA_ERR_ARG for a null or misaligned pointer (16 bytes; lse 4),
+ *   a bad dtype, shape or scale (as losa_sparse_attn), a pattern not
+ *   prepared, a workspace too small, a current device other than the
+ *   pattern's; LOSA_ERR_UNSUPPORTED, LOSA_ERR_CUDA.
+ */
+int losa_sparse_attn_bwd(const void* q, const void* k, const void* v, int in_dtype,
+                         const void* o, int o_dtype, const float* lse, const void* d_o,
+                         int do_dtype, int d, int L, float scale, const losa_pattern* p, void* dq,
+                         void* dk, void* dv, int out_dtype, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that losa_sparse_attn_bwd needs for this pattern, dtypes
+ * and head dim, or LOSA_ERR_ARG (negative). */
+int64_t losa_sparse_attn_bwd_workspace(const losa_pattern* p, int in_dtype, int do_dtype, int d);
+
+/*
+ * Rotary positions over the axes of a token grid (time, height, width for
+ * video; fewer axes for images or text), together with the change of layout
+ * between a model's projections and the attention calls.
+ */
+typedef enum {
+  LOSA_ROPE_INTERLEAVED = 0, /* pair i of an axis is its features 2i, 2i + 1 */
+  LOSA_ROPE_HALVES = 1       /* its features i, i + dim/2 */
+} losa_rope_pairing;
+
+typedef struct {
+  int n_axes;      /* 1 to 3, outermost first */
+  int grid[3];     /* tokens along each axis; their product is L - n_text */
+  int dim[3];      /* features each axis turns: even, >= 2, in this order from
+                      feature 0; features past their sum are not turned */
+  int start[3];    /* position of each axis's first token */
+  double scale[3]; /* factor on an axis's positions (1: none) */
+  double theta;    /* pair i of axis a turns by position * theta^(-2i/dim[a]) */
+  int n_text;      /* leading tokens that are not turned */
+  int pairing;     /* losa_rope_pairing */
+} losa_rope_spec;
+
+/*
+ * losa_rope_pack - turns Q and K by their tokens' positions and lays Q, K
+ * and V out for the attention calls, in one pass over memory.
+ *
+ *   q, k, v   [B, L, H, d] device, in_dtype, with element strides
+ *             strides[9] = (batch, token, head) of q, of k, of v; features
+ *             are adjacent (a fused projection's views need no copy). Any of
+ *             the three may be NULL together with its output.
+ *   q_out, k_out, v_out  [B, H, L_pad, d] contiguous, out_dtype; q and k
+ *             turned, v as it is; rows >= L are 0. They must not overlap the
+ *             inputs.
+ *   positions [B, L, n_axes] int32 device, contiguous, or NULL: positions
+ *             listed per token instead of spec's grid and start (scale still
+ *             applies; the first n_text tokens are not turned).
+ *   Angles are reduced in 64 bits, so far positions keep their precision;
+ *   values are turned in fp32 and rounded once.
+ *   Neither allocates nor synchronises.
+ *   Returns LOSA_ERR_ARG for: null spec, strides or all of q, k, v, an input
+ *   without its output or the reverse, a dtype out of range, B, H, L < 1,
+ *   L_pad < L, L_pad - L >= 128, d not in {64, 128}, B*H > 65535, a pointer
+ *   not aligned to its elements, a stride < 0 or > 2^40 / extent, a spec out of the
+ *   ranges above (theta and scale finite, theta > 0, n_text <= L);
+ *   LOSA_ERR_UNSUPPORTED, LOSA_ERR_CUDA.
+ */
+int losa_rope_pack(const void* q, const void* k, const void* v, int in_dtype,
+                   const int64_t* strides, int B, int H, int L, int L_pad, int d,
+                   const losa_rope_spec* spec, const int32_t* positions, void* q_out,
+                   void* k_out, void* v_out, int out_dtype, void* stream);
+
+/*
+ * losa_rope_unpack - the way back, which is also losa_rope_pack's gradient:
+ * q, k, v [B, H, L_pad, d] contiguous, in_dtype (gradients of packed Q, K,
+ * V), to q_out, k_out, v_out [B, L, H, d], out_dtype, strides as above, q
+ * and k turned by the negative angle. Rows >= L are not read. An attention
+ * output goes back to token order as v alone. Elements of an output must not
+ * overlap each other (refused) nor anything else.
+ *   Returns as losa_rope_pack does.
+ */
+int losa_rope_unpack(const void* q, const void* k, const void* v, int in_dtype, int B, int H,
+                     int L, int L_pad, int d, const losa_rope_spec* spec,
+                     const int32_t* positions, void* q_out, void* k_out, void* v_out,
+                     int out_dtype, const int64_t* strides, void* stream);
+
 /* Largest B*H*n_blocks that losa_select_noalloc accepts. */
 #define LOSA_NOALLOC_MAX_ROWS 65536
 

@@ -1,0 +1,360 @@
+"""losa_sparse_attn_bwd against the gradient's formula in 64 bits, and the
+forward pass's own differences.
+
+The reference takes the call's own inputs (O and lse among them) in 64 bits.
+Tolerances are error bounds, value by value, with u = 2^-24 (half a step of
+fp32), v = 2^-8 (half a step of bf16) on the tensor-core path and 0 on the
+fp32 one, and |.| products for sums (a sum of n terms in fp32 is within n u of
+the sum of their sizes):
+  scores   es = (d + 4) u scale |q||k|^T + 4 u |x| + 4 u |lse|, x the exponent
+  P        eP = P (expm1(es) + 4 u); rounded to bf16 as an operand: + v P
+  dP - D   ed = (d + 4) u (|dO||V|^T + |dO|.|O|)
+  dS       eS = eP' |dP - D| + P ed; rounded: + v |dS|
+  dV       sum(eP |dO|) + (n + 8) u sum(P |dO|),  dQ, dK likewise of dS,
+plus half a step of the result's type. eP' is eP without the operand's
+rounding: dS is formed from the unrounded P.
+"""
+import math
+
+import pytest
+import torch
+
+import workloads as W
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+V = 2.0 ** -8
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def losa():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    import block_sparse_attention_losa_b200 as m
+    return m
+
+
+def make_mask(bh, n, density, g, unused=False):
+    """Kept blocks, ragged from row to row, at least one each; with `unused`
+    the second key block is kept by no query block."""
+    mask = torch.rand(bh, n, n, generator=g) < density * (0.3 + 1.4 * torch.rand(bh, n, 1,
+                                                                               generator=g))
+    mask[:, torch.arange(n), torch.randint(0, n, (n,), generator=g)] = True
+    if unused and n > 1:
+        mask[:, :, 1] = False
+        mask[:, :, 0] |= ~mask.any(-1)
+    return mask
+
+
+def pattern_of(losa, mask, B, H, block):
+    row_ptr = torch.zeros(mask.shape[0] * mask.shape[1] + 1, dtype=torch.int32)
+    row_ptr[1:] = mask.sum(-1).flatten().cumsum(0)
+    return losa.import_pattern(row_ptr, mask.nonzero()[:, 2], B, H, mask.shape[1],
+                               block).prepare_backward()
+
+
+def token_mask(mask, block, L):
+    return mask.repeat_interleave(block, 1).repeat_interleave(block, 2)[:, :L, :L]
+
+
+def forward64(q, k, v, keep, scale):
+    s = (q @ k.transpose(1, 2)) * scale
+    s = torch.where(keep, s, -math.inf)
+    lse = torch.logsumexp(s, -1)
+    return torch.exp(s - lse[..., None]) @ v, lse
+
+
+def reference(q, k, v, o, lse, do, keep, scale, rounded):
+    """Gradients in 64 bits ([BH, L, d] each) and their error bounds."""
+    d, L = q.shape[2], q.shape[1]
+    r = V if rounded else 0.0
+    t = lambda x: x.transpose(1, 2)
+    x = (q @ t(k)) * scale - lse[..., None]
+    p = torch.where(keep, torch.exp(x), 0.0)
+    es = (d + 4) * U * scale * (q.abs() @ t(k.abs())) + 4 * U * (x.abs() + lse.abs()[..., None])
+    ep = p * (torch.expm1(es) + 4 * U)
+    dd = (do @ t(v)) - (do * o).sum(-1, keepdim=True)
+    ed = (d + 4) * U * (do.abs() @ t(v.abs()) + (do * o).abs().sum(-1, keepdim=True))
+    ds = p * dd
+    es_ = ep * dd.abs() + p * ed
+    es_ = es_ + r * (ds.abs() + es_)
+    ep = ep + r * (p + ep)
+    n = (L + 8) * U
+    return [(ds @ k * scale, (es_ @ k.abs() + n * (ds.abs() @ k.abs())) * scale),
+            (t(ds) @ q * scale, (t(es_) @ q.abs() + n * (t(ds.abs()) @ q.abs())) * scale),
+            (t(p) @ do, t(ep) @ do.abs() + n * (t(p) @ do.abs()))]
+
+
+def close(got, ref, tol, L, names=("dq", "dk", "dv")):
+    for name, g, (r, e) in zip(names, got, zip(ref, tol)):
+        step = V if g.dtype == BF else U
+        e = e * (1 + step) + step * r.abs()
+        x = g.flatten(0, 1)
+        worst = ((x[:, :L].double() - r).abs() - e).max().item()
+        assert worst <= 0, (name, worst, r.abs().max().item())
+        assert (x[:, L:] == 0).all(), name
+
+
+def inputs(B, H, L, Lp, d, dtype, o_dtype, do_dtype, mask, block, seed, spread=1.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(4, B * H, L, d, generator=g).to("cuda")
+    x[0] *= spread
+    q, k, v = (t.to(dtype).double() for t in x[:3])
+    do = x[3].to(do_dtype).double()
+    keep = token_mask(mask, block, L).cuda()
+    scale = 1 / math.sqrt(d)
+    o, lse = forward64(q, k, v, keep, scale)
+    o, lse = o.to(o_dtype).double(), lse.float().double()
+
+    def padded(t, dt, fill=float("nan")):  # rows >= L must not matter
+        y = torch.full((B * H, Lp) + t.shape[2:], fill, device="cuda", dtype=dt)
+        y[:, :L] = t.to(dt)
+        return y.view(B, H, Lp, *t.shape[2:])
+
+    args = [padded(q, dtype), padded(k, dtype), padded(v, dtype), padded(o, o_dtype),
+            padded(lse, F32, -math.inf), padded(do, do_dtype)]
+    # The tensor cores read a fp32 dO rounded to bf16.
+    seen = do.to(BF).double() if dtype == BF else do
+    pairs = reference(q, k, v, o, lse, seen, keep, scale, dtype == BF)
+    return args, [p[0] for p in pairs], [p[1] for p in pairs]
+
+
+SHAPES = [  # B, H, d, L, block, density
+    (1, 1, 64, 1, 32, 1.0), (1, 2, 128, 1, 128, 1.0), (2, 1, 128, 31, 32, 1.0),
+    (1, 2, 64, 33, 32, 0.5), (1, 1, 128, 64, 64, 1.0), (1, 2, 128, 129, 128, 0.6),
+    (1, 2, 64, 256, 32, 0.5), (2, 3, 128, 390, 64, 0.4), (1, 2, 64, 500, 128, 0.5),
+    (1, 1, 128, 721, 32, 0.15), (1, 2, 64, 1000, 64, 0.3), (3, 1, 128, 1025, 128, 0.7),
+    (1, 1, 64, 1100, 32, 0.05),
+]
+TYPES = [(BF, F32, BF, BF), (BF, BF, BF, F32), (BF, F32, F32, BF), (F32, F32, F32, F32),
+         (F32, BF, BF, F32), (F32, F32, F32, BF)]  # in, o, do, out
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("types", TYPES)
+def test_gradients(losa, shape, types):
+    B, H, d, L, block, density = shape
+    dtype, o_dtype, do_dtype, out_dtype = types
+    n = -(-L // block)
+    mask = make_mask(B * H, n, density, torch.Generator().manual_seed(L), unused=L % 2 == 0)
+    pat = pattern_of(losa, mask, B, H, block)
+    args, ref, tol = inputs(B, H, L, n * block, d, dtype, o_dtype, do_dtype, mask, block, L + d)
+    got = losa.sparse_attn_bwd(*args, L, pat, out_dtype=out_dtype)
+    losa.check_status()
+    assert all(t.dtype == out_dtype for t in got)
+    close(got, ref, tol, L)
+    if n > 1 and L % 2 == 0:  # a key block that nothing keeps
+        for t in got[1:]:
+            assert (t[:, :, block:2 * block] == 0).all()
+    again = losa.sparse_attn_bwd(*args, L, pat, out_dtype=out_dtype)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    pat.close()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("spread", [1e-3, 30.0])
+def test_flat_and_peaked_rows(losa, dtype, spread):
+    """Scores that are all alike, and rows where one key takes everything."""
+    B, H, d, L, block = 1, 2, 128, 300, 64
+    mask = make_mask(2, 5, 0.6, torch.Generator().manual_seed(1))
+    pat = pattern_of(losa, mask, B, H, block)
+    args, ref, tol = inputs(B, H, L, 320, d, dtype, F32, dtype, mask, block, 5, spread)
+    close(losa.sparse_attn_bwd(*args, L, pat), ref, tol, L)
+    losa.check_status()
+
+
+@pytest.mark.parametrize("block,d", [(32, 64), (64, 128), (128, 128), (32, 128), (128, 64)])
+def test_lists_by_key_are_the_transposed_pattern(losa, block, d):
+    B, H, n = 2, 2, 21
+    mask = make_mask(4, n, 0.3, torch.Generator().manual_seed(block), unused=True)
+    pat = pattern_of(losa, mask, B, H, block)
+    ex = pat.export_backward()
+    per, tiles = 128 // block, -(-n * block // 128)
+    counts = []
+    for t in range(4 * tiles):
+        bh, kt = divmod(t, tiles)
+        m = mask[bh][:, kt * per:(kt + 1) * per]
+        want = [(I, sum(int(x) << c for c, x in enumerate(m[I].tolist())))
+                for I in range(n) if m[I].any()]
+        got = ex["key_entry"][ex["key_ptr"][t]:ex["key_ptr"][t + 1]].tolist()
+        assert [(e & 0xFFFF, e >> 16) for e in got] == want
+        counts.append(len(want))
+    order = ex["key_order"].tolist()
+    assert sorted(order) == list(range(4 * tiles))
+    for a, b in zip(order, order[1:]):
+        assert a // tiles < b // tiles or (a // tiles == b // tiles and counts[a] >= counts[b])
+
+
+def test_long_ragged_pattern(losa):
+    """Many iterations per tile, several key tiles, a ragged end; bf16."""
+    B, H, d, L, block = 1, 1, 128, 5003, 64
+    n = -(-L // block)
+    mask = make_mask(1, n, 0.5, torch.Generator().manual_seed(9))
+    pat = pattern_of(losa, mask, B, H, block)
+    args, ref, tol = inputs(B, H, L, n * block, d, BF, F32, BF, mask, block, 11)
+    close(losa.sparse_attn_bwd(*args, L, pat), ref, tol, L)
+    losa.check_status()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_against_differences_of_the_forward_call(losa, dtype):
+    """The loss <O, R> of the forward call moves as the gradients say: a
+    central difference along random directions. bf16 / tf32 forward outputs
+    carry rounding noise, so the step is large and the bound is the noise over
+    the step: O's errors are below 1e-2 each (the forward's own tolerance)
+    but of random sign; their sum against R (norm |R|) over a step h stays
+    below 6 * 1e-3 |R| / h, 1e-3 being the forward's bound on their mean size;
+    the quadratic and cubic terms are below 5 % of the derivative's scale."""
+    wl = W.custom("bwd", 2, 64, (2, 8, 16), 32, text_tokens=3, amplitude=1.0, seed=77)
+    L = wl.seq_len
+    q, k, v = (t.cuda() for t in W.generate(wl, dtype=F32))
+    q, k, v = (t.to(dtype) for t in (q, k, v))
+    _, _, mass = losa.dense_mass(q, k, v, L, 32)
+    pat = losa.select(mass, 32, 0.95).prepare_backward()
+    g = torch.Generator("cuda").manual_seed(2)
+    R = torch.randn(q.shape, generator=g, device="cuda").to(dtype)
+    R[:, :, L:] = 0
+    o, lse = losa.sparse_attn(q, k, v, L, pat)
+    grads = losa.sparse_attn_bwd(q, k, v, o, lse, R, L, pat, out_dtype=F32)
+    h = 0.25
+    for i in range(3):
+        w = torch.randn(q.shape, generator=g, device="cuda")
+        w[:, :, L:] = 0
+        w *= 4.0 / w.norm()
+        ends = []
+        for sign in (1, -1):
+            x = [q, k, v]
+            x[i] = (x[i].float() + sign * h * w).to(dtype)
+            step = x[i].double() - (q, k, v)[i].double()
+            ends.append(((losa.sparse_attn(*x, L, pat)[0].double() * R.double()).sum(), step))
+        moved = ends[0][1] - ends[1][1]
+        want = (grads[i].double() * moved).sum()
+        got = ends[0][0] - ends[1][0]
+        size = (grads[i].double().norm() * moved.norm()).item()
+        assert (got - want).abs().item() <= 12e-3 * R.double().norm().item() + 0.05 * size
+
+
+def test_training_step_through_rope_and_graph(losa):
+    """pack, forward, backward and unpack as a training step runs them: the
+    gradients with respect to the token-major projections against a plain
+    formulation's, and the captured step's bits against the eager one's."""
+    B, H, d, grid, block, L = 1, 3, 128, (3, 10, 13), 64, 390
+    rope = losa.Rope(grid, (44, 42, 42))
+    g = torch.Generator("cuda").manual_seed(4)
+    n = -(-L // block)
+    mask = make_mask(H, n, 0.5, torch.Generator().manual_seed(6))
+    pat = pattern_of(losa, mask, B, H, block)
+    x = torch.randn(B, L, 3, H, d, generator=g, device="cuda").to(BF)
+    dout = torch.randn(B, L, H, d, generator=g, device="cuda").to(BF)
+
+    def step(x, dout):
+        q, k, v = losa.rope_pack(*x.unbind(2), block, rope)
+        o, lse = losa.sparse_attn(q, k, v, L, pat)
+        out = losa.rope_unpack(None, None, o, L, rope, out_dtype=BF)[2]
+        do = losa.rope_pack(None, None, dout, block, rope)[2]
+        grads = losa.sparse_attn_bwd(q, k, v, o, lse, do, L, pat)
+        dx = torch.empty_like(x)
+        losa.rope_unpack(*grads, L, rope, out=dx.unbind(2))
+        return out, dx
+
+    out, dx = step(x, dout)
+    losa.check_status()
+    # Plain, in 64 bits and on the unrounded path from x.
+    y = x.double().requires_grad_()
+    pos = torch.stack(torch.meshgrid(*(torch.arange(m, device="cuda") for m in grid),
+                                     indexing="ij"), -1).reshape(-1, 3).double()
+    ang = torch.cat([pos[:, a, None] * 10000.0 ** (-torch.arange(0, m, 2, device="cuda") / m)
+                     for a, m in enumerate((44, 42, 42))], 1)[None, :, None]
+    qkv = torch.view_as_complex(y.unflatten(-1, (d // 2, 2)))
+    turn = torch.polar(torch.ones_like(ang), ang)
+    q, k = (torch.view_as_real(qkv[:, :, i] * turn).flatten(-2).transpose(1, 2) for i in (0, 1))
+    v = y[:, :, 2].transpose(1, 2)
+    keep = token_mask(mask, block, L).cuda()[None]
+    s = torch.where(keep, q @ k.transpose(2, 3) / math.sqrt(d), -math.inf)
+    ref = (torch.softmax(s, -1) @ v).transpose(1, 2)
+    ref.backward(dout.double())
+    # Roundings to bf16 on the way of a gradient: q and k, P, dS, dq/dk, dx,
+    # each at most 2^-8 of its value; they add as norms, and q and k's also
+    # through the scores (|s| up to 5 here, e^(5 * 2^-8)): below 8 half steps.
+    rel = lambda a, b: ((a.double() - b).norm() / b.norm()).item()
+    assert rel(out, ref) <= 8 * V
+    assert rel(dx, y.grad) <= 8 * V
+    static, sd = torch.zeros_like(x), torch.zeros_like(dout)
+    graphs = []
+    for _ in range(2):  # two captured steps, each with its own memory
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = step(static, sd)
+        graphs.append((graph, got))
+    static.copy_(x)
+    sd.copy_(dout)
+    for graph, _ in graphs:
+        graph.replay()
+    for _, (o2, dx2) in graphs:
+        assert torch.equal(o2, out) and torch.equal(dx2, dx)
+
+
+def test_two_streams_at_once(losa):
+    B, H, d, L, block = 1, 4, 128, 1000, 64
+    mask = make_mask(4, 16, 0.5, torch.Generator().manual_seed(8))
+    pat = pattern_of(losa, mask, B, H, block)
+    a, _, _ = inputs(B, H, L, 1024, d, BF, F32, BF, mask, block, 21)
+    b, _, _ = inputs(B, H, L, 1024, d, BF, F32, BF, mask, block, 22)
+    want = [losa.sparse_attn_bwd(*x, L, pat) for x in (a, b)]
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = [losa.sparse_attn_bwd(*x, L, pat, stream=s) for x, s in zip((a, b), side)]
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(x, y) for x, y in zip(w, g))
+
+
+def test_given_outputs_and_workspace(losa):
+    B, H, d, L, block = 1, 2, 64, 200, 32
+    mask = make_mask(2, 7, 0.5, torch.Generator().manual_seed(3))
+    pat = pattern_of(losa, mask, B, H, block)
+    args, ref, tol = inputs(B, H, L, 224, d, BF, BF, BF, mask, block, 2)
+    out = [torch.full(args[0].shape, 9.0, device="cuda") for _ in range(3)]
+    need = losa.lib().losa_sparse_attn_bwd_workspace(pat.handle, 0, 0, d)
+    ws = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")
+    got = losa.sparse_attn_bwd(*args, L, pat, dq=out[0], dk=out[1], dv=out[2], workspace=ws)
+    assert all(a.data_ptr() == b.data_ptr() for a, b in zip(out, got))
+    assert (ws[need:] == 255).all()
+    close(got, ref, tol, L)
+
+
+def test_refusals(losa):
+    B, H, d, L, block = 1, 2, 64, 200, 32
+    mask = make_mask(2, 7, 0.5, torch.Generator().manual_seed(3))
+    pat = pattern_of(losa, mask, B, H, block)
+    q, k, v, o, lse, do = inputs(B, H, L, 224, d, BF, BF, BF, mask, block, 2)[0]
+    for change in (dict(o=o[:, :, :200]), dict(lse=lse.double()), dict(lse=lse[:, :, :200]),
+                   dict(do=do.transpose(0, 1)), dict(q=q[:, :1]), dict(do=do.cpu()),
+                   dict(dq=o.float(), dk=o), dict(dv=o[..., ::2]), dict(q=q.float()),
+                   dict(workspace=torch.empty(1 << 20))):
+        a = dict(q=q, k=k, v=v, o=o, lse=lse, do=do, L=L, pattern=pat)
+        a.update(change)
+        with pytest.raises(ValueError):
+            losa.sparse_attn_bwd(**a)
+    with pytest.raises(TypeError):
+        losa.sparse_attn_bwd(q, k, v, o.half(), lse, do, L, pat)
+    for change in (dict(L=192), dict(L=225), dict(L=0), dict(scale=0.0),
+                   dict(scale=float("nan")),
+                   dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))):
+        a = dict(q=q, k=k, v=v, o=o, lse=lse, do=do, L=L, pattern=pat)
+        a.update(change)
+        with pytest.raises(losa.LosaError):
+            losa.sparse_attn_bwd(**a)
+    fresh = losa.import_pattern(*(pat.export("cpu")[x] for x in ("row_ptr", "col_idx")), B, H, 7,
+                                block)
+    with pytest.raises(losa.LosaError):  # not prepared
+        losa.sparse_attn_bwd(q, k, v, o, lse, do, L, fresh)
+    with pytest.raises(losa.LosaError):
+        fresh.export_backward()
+    fresh.prepare_backward().prepare_backward()  # twice is once
+    losa.sparse_attn_bwd(q, k, v, o, lse, do, L, fresh)
+    losa.check_status()
+    fresh.close()
+    with pytest.raises(ValueError):
+        losa.sparse_attn_bwd(q, k, v, o, lse, do, L, fresh)
