@@ -20,7 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "liblosa.so")
 OBJ = os.path.join(HERE, "_build")
 SOURCES = ["losa_api.cu", "losa_attention.cu", "losa_select.cu", "losa_rope.cu",
-           "losa_backward.cu"]
+           "losa_backward.cu", "losa_backward_mma.cu"]
 HEADERS = ["losa_device.cuh", "losa_attention.cuh", "losa_cut.cuh", "losa_internal.h"]
 
 

@@ -16,6 +16,8 @@ namespace losa {
 // Wait limit of the attention kernels' mbarrier waits, in SM cycles.
 std::atomic<long long> g_wait_limit{kWaitLimitCycles};
 
+long long wait_limit() { return g_wait_limit.load(); }
+
 void set_wait_limit(long long cycles) {
   g_wait_limit.store(cycles > 0 ? cycles : kWaitLimitCycles);
 }
@@ -36,16 +38,18 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
   return fn;
 }
 
+}  // namespace
+
 // [BH, L_pad, d] bf16 (esz 2) or fp32 (esz 4) viewed as a 3D tensor (d
 // innermost), loaded in 128-byte-wide slabs (64 bf16 or 32 fp32 columns) of
 // `box_rows` rows with the 128-byte swizzle the MMA descriptors expect: of
 // 16-byte atoms, or of 32-byte atoms (atom32) for an fp32 operand the tf32
-// MMAs read MN-major (V). Rows past L_pad read as zero.
-bool make_map(CUtensorMap* map, const void* base, int BH, int L_pad, int d, int box_rows,
-              int esz, bool atom32 = false) {
+// MMAs read MN-major (V). Rows past `rows` (<= L_pad) read as zero.
+bool make_slab_map(CUtensorMap* map, const void* base, int BH, int rows, int L_pad, int d,
+                   int box_rows, int esz, bool atom32) {
   auto enc = get_encode_fn();
   if (!enc) return false;
-  cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(L_pad), cuuint64_t(BH)};
+  cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(rows), cuuint64_t(BH)};
   cuuint64_t strides[2] = {cuuint64_t(d) * esz, cuuint64_t(L_pad) * d * esz};
   cuuint32_t box[3] = {cuuint32_t(128 / esz), cuuint32_t(box_rows), 1};
   cuuint32_t estr[3] = {1, 1, 1};
@@ -55,6 +59,13 @@ bool make_map(CUtensorMap* map, const void* base, int BH, int L_pad, int d, int 
                    atom32 ? CU_TENSOR_MAP_SWIZZLE_128B_ATOM_32B : CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+namespace {
+
+bool make_map(CUtensorMap* map, const void* base, int BH, int L_pad, int d, int box_rows,
+              int esz, bool atom32 = false) {
+  return make_slab_map(map, base, BH, L_pad, L_pad, d, box_rows, esz, atom32);
 }
 
 template <int D, int BN, int NSK, int NSV, bool kDense, bool kOutBf16, int BLK, bool kTf32,

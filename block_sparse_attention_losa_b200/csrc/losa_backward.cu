@@ -47,10 +47,29 @@ __device__ __forceinline__ void load_row(const void* base, bool bf16, size_t row
   }
 }
 
+// Three bf16 terms whose sum is x to 24 bits, as the first columns of a
+// 16-column operand row (the other columns 0).
+__device__ __forceinline__ uint4 split3(float x) {
+  const uint32_t h = pack_bf16x2(x, 0.f) & 0xffffu;
+  const float r1 = x - __uint_as_float(h << 16);
+  const uint32_t m = pack_bf16x2(r1, 0.f) & 0xffffu;
+  const float r2 = r1 - __uint_as_float(m << 16);
+  const uint32_t l = pack_bf16x2(r2, 0.f) & 0xffffu;
+  return make_uint4(h | (m << 16), l, 0u, 0u);
+}
+
+// The bf16 path's further operand rows, which carry -lse / scale and -D into
+// its products: 8-row groups of two 8 x 16-byte core matrices each.
+struct AugRows {
+  uint4 *q, *d_o;  // null on the fp32 path
+  const float* lse;
+  float inv_scale;
+};
+
 template <int D>
 __global__ void __launch_bounds__(256)
     delta_kernel(const void* o, bool o_bf16, const void* d_o, bool do_bf16, int64_t rows,
-                 int L, int L_pad, float* delta, uint16_t* rounded) {
+                 int L, int L_pad, float* delta, uint16_t* rounded, const AugRows aug) {
   const int lane = threadIdx.x & 31;
   const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (row >= rows) return;
@@ -74,13 +93,27 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   if (lane == 0) delta[row] = sum;
+  if (aug.q && lane < 4) {
+    // Lanes 0, 1: the row's two halves of q's columns; 2, 3: of dO's. Padded
+    // rows get a score far below any other, so their weight is 0; values are
+    // kept inside bf16's range.
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (lane == 0) {
+      const float a = row % L_pad < L ? -aug.lse[row] * aug.inv_scale : -3e38f;
+      x = split3(fminf(fmaxf(a, -3e38f), 3e38f));
+    } else if (lane == 2) {
+      x = split3(fminf(fmaxf(-sum, -3e38f), 3e38f));
+    }
+    (lane < 2 ? aug.q : aug.d_o)[(row >> 3) * 16 + (lane & 1) * 8 + (row & 7)] = x;
+  }
 }
 
 // ------------------------------------------------------------------ fp32
 
 struct SimtParams {
-  const void *q, *k, *v, *d_o;
-  bool in_bf16, do_bf16, out_bf16;
+  const float *q, *k, *v;
+  const void* d_o;
+  bool do_bf16, out_bf16;
   const float *lse, *delta;
   int L, L_pad, n_qt, block;
   float scale;
@@ -146,8 +179,8 @@ __global__ void __launch_bounds__(kSimtThreads)
           (r0 >= 0 && r0 + r < p.L) ? load_value(src, bf16, (base + r0 + r) * D + c) : 0.f;
     }
   };
-  fill(sm.x, kKeys ? p.k : p.q, p.in_bf16, own0, 0, kSimtRows);
-  fill(sm.x2, kKeys ? p.v : p.d_o, kKeys ? p.in_bf16 : p.do_bf16, own0, 0, kSimtRows);
+  fill(sm.x, kKeys ? p.k : p.q, false, own0, 0, kSimtRows);
+  fill(sm.x2, kKeys ? p.v : p.d_o, kKeys ? false : p.do_bf16, own0, 0, kSimtRows);
 
   float acc[4][NC * 4] = {}, acc2[kKeys ? 4 : 1][NC * 4] = {};
   float own_lse[4], own_delta[4];
@@ -186,8 +219,8 @@ __global__ void __launch_bounds__(kSimtThreads)
     __syncthreads();  // the step before has read y, y2, p and ds
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      fill(sm.y, kKeys ? p.q : p.k, p.in_bf16, row0[s], 32 * s, 32);
-      fill(sm.y2, kKeys ? p.d_o : p.v, kKeys ? p.do_bf16 : p.in_bf16, row0[s], 32 * s, 32);
+      fill(sm.y, kKeys ? p.q : p.k, false, row0[s], 32 * s, 32);
+      fill(sm.y2, kKeys ? p.d_o : p.v, kKeys ? p.do_bf16 : false, row0[s], 32 * s, 32);
     }
     __syncthreads();
     // Scores and dP: own rows 4 ty + a, step rows tx + 16 c.
@@ -293,35 +326,55 @@ cudaError_t run_simt(const SimtParams& p, int64_t tiles, cudaStream_t stream) {
 
 }  // namespace
 
-// D, and a bf16 copy of a fp32 dO for bf16 inputs.
+namespace {
+// Offsets of a call's workspace: D, the bf16 path's further operand rows and
+// its bf16 copy of a fp32 dO. Rows come in multiples of 32, so each part is
+// aligned to 128 bytes.
+struct Workspace {
+  size_t q_aug, do_aug, rounded, bytes;
+  Workspace(const losa_pattern* p, int d, bool in_bf16, bool do_bf16) {
+    const size_t rows = size_t(p->B) * p->H * p->n_blocks * p->block;
+    q_aug = rows * 4;
+    do_aug = q_aug + (in_bf16 ? rows * 32 : 0);
+    rounded = do_aug + (in_bf16 ? rows * 32 : 0);
+    bytes = rounded + (in_bf16 && !do_bf16 ? rows * d * 2 : 0);
+  }
+};
+}  // namespace
+
 size_t backward_workspace(const losa_pattern* p, int d, bool in_bf16, bool do_bf16) {
-  const size_t rows = size_t(p->B) * p->H * p->n_blocks * p->block;
-  return rows * 4 + (in_bf16 && !do_bf16 ? rows * d * 2 : 0);
+  return Workspace(p, d, in_bf16, do_bf16).bytes;
 }
 
 cudaError_t launch_backward(const BackwardCall& c, cudaStream_t stream) {
   const losa_pattern* pat = c.p;
   const int L_pad = pat->n_blocks * pat->block;
   const int64_t rows = int64_t(pat->B) * pat->H * L_pad;
-  float* delta = static_cast<float*>(c.workspace);
+  const Workspace at(pat, c.d, c.in_bf16, c.do_bf16);
+  char* ws = static_cast<char*>(c.workspace);
+  float* delta = reinterpret_cast<float*>(ws);
   uint16_t* rounded =
-      c.in_bf16 && !c.do_bf16 ? static_cast<uint16_t*>(c.workspace) + rows * 2 : nullptr;
+      c.in_bf16 && !c.do_bf16 ? reinterpret_cast<uint16_t*>(ws + at.rounded) : nullptr;
+  AugRows aug{};
+  if (c.in_bf16)
+    aug = {reinterpret_cast<uint4*>(ws + at.q_aug), reinterpret_cast<uint4*>(ws + at.do_aug), c.lse,
+           1.f / c.scale};
   const unsigned grid = unsigned((rows + 7) / 8);
-  if (c.d == 64)
-    delta_kernel<64><<<grid, 256, 0, stream>>>(c.o, c.o_bf16, c.d_o, c.do_bf16, rows, c.L, L_pad,
-                                               delta, rounded);
-  else
-    delta_kernel<128><<<grid, 256, 0, stream>>>(c.o, c.o_bf16, c.d_o, c.do_bf16, rows, c.L, L_pad,
-                                                delta, rounded);
+  (c.d == 64 ? delta_kernel<64> : delta_kernel<128>)<<<grid, 256, 0, stream>>>(
+      c.o, c.o_bf16, c.d_o, c.do_bf16, rows, c.L, L_pad, delta, rounded, aug);
   cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
+  if (c.in_bf16)
+    return launch_backward_mma(c, {rounded ? rounded : c.d_o, delta,
+                                   reinterpret_cast<const uint16_t*>(ws + at.q_aug),
+                                   reinterpret_cast<const uint16_t*>(ws + at.do_aug)},
+                               stream);
   SimtParams p{};
-  p.q = c.q;
-  p.k = c.k;
-  p.v = c.v;
-  p.d_o = rounded ? rounded : c.d_o;
-  p.in_bf16 = c.in_bf16;
-  p.do_bf16 = c.do_bf16 || rounded;
+  p.q = static_cast<const float*>(c.q);
+  p.k = static_cast<const float*>(c.k);
+  p.v = static_cast<const float*>(c.v);
+  p.d_o = c.d_o;
+  p.do_bf16 = c.do_bf16;
   p.out_bf16 = c.out_bf16;
   p.lse = c.lse;
   p.delta = delta;

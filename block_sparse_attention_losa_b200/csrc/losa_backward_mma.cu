@@ -1,0 +1,834 @@
+// losa_backward_mma.cu - the tensor-core kernels of losa_sparse_attn_bwd
+// (bf16 operands, fp32 accumulation in tensor memory): one for dK and dV,
+// which owns 128 key rows and walks the query blocks that keep them, and one
+// for dQ, which owns 128 query rows and walks the key blocks they keep.
+#include <algorithm>
+
+#include "losa_device.cuh"
+#include "losa_internal.h"
+
+namespace losa {
+namespace {
+
+constexpr int kBwdThreads = 384;
+constexpr int kTile = 128;  // rows a CTA owns, and rows of a step
+constexpr int kAugBytes = kTile * 32;
+
+struct BwdParams {
+  int L, L_pad, n_qt, n_tiles;
+  float scale, scale_log2;
+  const int *ptr, *entry, *order;
+  const float *lse, *delta;
+  const uint16_t *q_aug, *do_aug;
+  const void *q, *d_o;  // dQ kernel: its own rows
+  void *out0, *out1;    // dV, dK, or dQ
+  int* status;
+  long long wait_limit;
+};
+
+// cp.async.bulk of `bytes` (a multiple of 16, both sides 16-byte aligned).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_addr(dst)),
+      "l"(src), "r"(bytes), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// Matrix descriptor of a K-major operand of 16 bf16 columns without swizzle:
+// 8-row groups of 256 bytes (SBO), each two 8 x 16-byte core matrices 128
+// bytes apart (LBO).
+__device__ __forceinline__ uint64_t sdesc_aug(uint32_t saddr) {
+  return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(128 >> 4) << 16) |
+         (uint64_t(256 >> 4) << 32) | (1ull << 46);
+}
+
+__device__ __forceinline__ void tmem_ld_64(uint32_t taddr, float (&r)[64]) {
+  tmem_ld32(taddr, *reinterpret_cast<float(*)[32]>(&r[0]));
+  tmem_ld32(taddr + 32, *reinterpret_cast<float(*)[32]>(&r[32]));
+}
+
+// One arrival per warp: every lane's tensor-memory accesses are complete
+// (tcgen05.wait) and ordered before it.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// A wait of a whole warp, with one answer for all its lanes, so that none
+// goes on alone into the warp-wide tensor-memory accesses after a wait that
+// others gave up.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, w));
+}
+
+// Of every 16 column pairs, how many take exp2 on the FMA pipe.
+constexpr int kPolyPairs = 4;
+
+// e = 2^(x * c) of 32 values.
+__device__ __forceinline__ void exp2_scaled(float (&x)[32], float c) {
+  const f32x2 c2 = f2_make(c, c);
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    float a, b;
+    f2_split(f2_mul(f2_make(x[i], x[i + 1]), c2), a, b);
+    if ((i >> 1) < kPolyPairs) {
+      exp2_fma2(a, b, x[i], x[i + 1]);
+    } else {
+      x[i] = ex2_approx(a);
+      x[i + 1] = ex2_approx(b);
+    }
+  }
+}
+// e = 2^(x * c + o) of 32 values.
+__device__ __forceinline__ void exp2_shifted(float (&x)[32], float c, float o) {
+  const f32x2 c2 = f2_make(c, c), o2 = f2_make(o, o);
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    float a, b;
+    f2_split(f2_fma(f2_make(x[i], x[i + 1]), c2, o2), a, b);
+    if ((i >> 1) < kPolyPairs) {
+      exp2_fma2(a, b, x[i], x[i + 1]);
+    } else {
+      x[i] = ex2_approx(a);
+      x[i + 1] = ex2_approx(b);
+    }
+  }
+}
+
+// Stores 32 values as bf16 pairs over 16 columns.
+__device__ __forceinline__ void tmem_st_bf16(uint32_t taddr, const float (&x)[32]) {
+  uint32_t pk[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+  tmem_st16(taddr, pk);
+}
+
+// Writes one row's 32 accumulator columns, times f, to the result.
+template <bool kOutBf16>
+__device__ __forceinline__ void store_row32(void* out, size_t at, const float (&x)[32], float f) {
+  if constexpr (kOutBf16) {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
+#pragma unroll
+    for (int e = 0; e < 32; e += 8) {
+      uint4 w;
+      w.x = pack_bf16x2(x[e] * f, x[e + 1] * f);
+      w.y = pack_bf16x2(x[e + 2] * f, x[e + 3] * f);
+      w.z = pack_bf16x2(x[e + 4] * f, x[e + 5] * f);
+      w.w = pack_bf16x2(x[e + 6] * f, x[e + 7] * f);
+      dst[e / 8] = w;
+    }
+  } else {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+#pragma unroll
+    for (int e = 0; e < 32; e += 4)
+      dst[e / 4] = make_float4(x[e] * f, x[e + 1] * f, x[e + 2] * f, x[e + 3] * f);
+  }
+}
+template <bool kOutBf16>
+__device__ __forceinline__ void store_zero32(void* out, size_t at) {
+  const float zero[32] = {};
+  store_row32<kOutBf16>(out, at, zero, 0.f);
+}
+
+// ------------------------------------------------------------------ dK, dV
+
+// Shared memory of the dK/dV kernel: its K and V tiles, the constant operand
+// that adds lse and D, and a ring of steps (Q and dO tiles with their rows of
+// lse and D).
+template <int D> struct KeyLayout {
+  static constexpr int NS = D == 128 ? 2 : 4;  // stages
+  static constexpr int TILE_BYTES = kTile * D * 2;
+  static constexpr int OFF_K = 0;
+  static constexpr int OFF_V = OFF_K + TILE_BYTES;
+  static constexpr int OFF_Q = OFF_V + TILE_BYTES;
+  static constexpr int OFF_DO = OFF_Q + NS * TILE_BYTES;
+  static constexpr int OFF_QA = OFF_DO + NS * TILE_BYTES;
+  static constexpr int OFF_DA = OFF_QA + NS * kAugBytes;
+  static constexpr int OFF_ONE = OFF_DA + NS * kAugBytes;
+  static constexpr int OFF_BAR = OFF_ONE + kAugBytes;
+  static constexpr int N_BARS = 4 * NS + 8;
+  static constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
+  static constexpr int BYTES = OFF_MISC + 16;
+  // 1 KB of slack for alignment; above 116 KB, so that one CTA runs per SM
+  // (each allocates all 512 TMEM columns).
+  static constexpr int SMEM_ALLOC = BYTES + 1024;
+  static_assert(SMEM_ALLOC > 116 * 1024 && SMEM_ALLOC <= 227 * 1024, "shared memory");
+};
+
+// Scores are formed transposed (rows are keys), so that P^T and dS^T lie in
+// tensor memory as the A operands of dV and dK. The row constants lse_i and
+// D_i then run along the columns, where a thread would have to load one per
+// score; instead they enter the products: Q and dO get 16 further columns
+// that hold -lse_i / scale and -D_i as three bf16 terms each (24 bits), and
+// K and V matching columns of ones, so S^T arrives as q.k - lse / scale and
+// dP^T as dO.v - D for 1/8 of a product's time each.
+//
+// Per step j the MMA thread issues dV(j), S(j+1), dK(j), dP(j+1): the
+// softmax's first half (P from S) runs under dK(j-1) and dP(j), its second
+// (dS from P and dP) under dV(j) and S(j+1), with one buffer of each in the
+// 512 columns of tensor memory: S/P, dP/dS, dV, dK.
+//
+// Warps 0-7 hold the scores, thread t of a warp one key row and half the
+// query columns; warp 8 loads, warp 9 issues the MMAs.
+template <int D, int BLK, bool kOutBf16>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    bwd_key_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                   const BwdParams p) {
+  using Lay = KeyLayout<D>;
+  constexpr int NS = Lay::NS;
+  constexpr int EPI = kTile / BLK;  // list entries per step
+  constexpr int SLABS = D / 64;
+  constexpr uint32_t C_S = 0, C_DP = 128, C_DV = 256, C_DK = 256 + D;
+  constexpr uint32_t IDESC_S = idesc_bf16_f32(kTile, kTile, false, false);
+  constexpr uint32_t IDESC_G = idesc_bf16_f32(kTile, D, false, true);
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::OFF_BAR);
+  uint64_t* q_full = bars;             // [NS]
+  uint64_t* q_empty = q_full + NS;     // [NS]
+  uint64_t* do_full = q_empty + NS;    // [NS]
+  uint64_t* do_empty = do_full + NS;   // [NS]
+  uint64_t* kv_full = do_empty + NS;   // K and V
+  uint64_t* s_full = kv_full + 1;
+  uint64_t* dp_full = s_full + 1;
+  uint64_t* p_full = dp_full + 1;
+  uint64_t* ds_full = p_full + 1;
+  uint64_t* acc_full = ds_full + 1;
+  uint64_t* drain_bar = acc_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::OFF_MISC + 4);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int tile = p.order[blockIdx.x];
+  const int bh = tile / p.n_qt;
+  const int kt = tile - bh * p.n_qt;
+  const int e0 = p.ptr[tile];
+  const int n_ent = p.ptr[tile + 1] - e0;
+  const int n_it = (n_ent + EPI - 1) / EPI;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], 1);
+      mbar_init(&do_full[s], 1);
+      mbar_init(&do_empty[s], 1);
+    }
+    mbar_init(kv_full, 1);
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(p_full, 8);
+    mbar_init(ds_full, 8);
+    mbar_init(acc_full, 1);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  // The ones: columns 0 to 2 of every row.
+  for (int i = threadIdx.x; i < kAugBytes / 16; i += kBwdThreads) {
+    const bool first = (i & 15) < 8;  // the row group's first core matrix
+    reinterpret_cast<uint4*>(smem + Lay::OFF_ONE)[i] =
+        first ? make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  if (warp == 9) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtx wc{abort_flag, p.status, p.wait_limit};
+
+  if (warp == 8) {
+    // ================================================================ producer
+    if (lane == 0 && n_it > 0) {
+      tma_prefetch_map(&tm_k);
+      tma_prefetch_map(&tm_v);
+      tma_prefetch_map(&tm_q);
+      tma_prefetch_map(&tm_do);
+      mbar_arrive_expect_tx(kv_full, 2 * Lay::TILE_BYTES);
+#pragma unroll
+      for (int s = 0; s < SLABS; ++s) {
+        tma_load_3d(smem + Lay::OFF_K + s * (kTile * 128), &tm_k, kv_full, s * 64, kt * kTile, bh);
+        tma_load_3d(smem + Lay::OFF_V + s * (kTile * 128), &tm_v, kv_full, s * 64, kt * kTile, bh);
+      }
+      bool ok = true;
+      int loaded_q = 0, loaded_do = 0;
+      for (int j = 0; ok && j < n_it; ++j) {
+        const int st = j % NS;
+        const uint32_t parity = ((j / NS) & 1) ^ 1;
+        // Slots past the end of the list repeat its last entry; the softmax
+        // masks their columns.
+        int row[EPI];
+#pragma unroll
+        for (int e = 0; e < EPI; ++e)
+          row[e] = (p.entry[e0 + min(j * EPI + e, n_ent - 1)] & 0xFFFF) * BLK;
+        auto load = [&](const CUtensorMap* map, const uint16_t* aug, uint64_t* full, int off,
+                        int off_aug) {
+          mbar_arrive_expect_tx(full, Lay::TILE_BYTES + kAugBytes);
+#pragma unroll
+          for (int e = 0; e < EPI; ++e) {
+#pragma unroll
+            for (int s = 0; s < SLABS; ++s)
+              tma_load_3d(smem + off + st * Lay::TILE_BYTES + s * (kTile * 128) + e * (BLK * 128),
+                          map, full, s * 64, row[e], bh);
+            bulk_load(smem + off_aug + st * kAugBytes + e * (BLK * 32),
+                      aug + (size_t(bh) * p.L_pad + row[e]) * 16, BLK * 32, full);
+          }
+        };
+        if (!(ok = mbar_wait(&q_empty[st], parity, wc))) break;
+        load(&tm_q, p.q_aug, &q_full[st], Lay::OFF_Q, Lay::OFF_QA);
+        ++loaded_q;
+        if (!(ok = mbar_wait(&do_empty[st], parity, wc))) break;
+        load(&tm_do, p.do_aug, &do_full[st], Lay::OFF_DO, Lay::OFF_DA);
+        ++loaded_do;
+      }
+      if (!ok) {
+        // Aborted: let the copies in flight land before the CTA ends.
+        mbar_wait_drain(kv_full, 0);
+        for (int i = max(loaded_q - NS, 0); i < loaded_q; ++i)
+          mbar_wait_drain(&q_full[i % NS], (i / NS) & 1);
+        for (int i = max(loaded_do - NS, 0); i < loaded_do; ++i)
+          mbar_wait_drain(&do_full[i % NS], (i / NS) & 1);
+      }
+    }
+  } else if (warp == 9) {
+    // ================================================================ MMA issuer
+    if (lane == 0 && n_it > 0) {
+      const uint32_t base = smem_addr(smem);
+      // D[col] = own (A) * step's rows (B)^T + ones * aug^T
+      auto issue_scores = [&](uint32_t col, int own, int off, int off_aug, int st) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t o = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+          umma_bf16_ss(tmem + col, sdesc_sw128(base + own + o, 16, 1024),
+                       sdesc_sw128(base + off + st * Lay::TILE_BYTES + o, 16, 1024), IDESC_S,
+                       kk > 0 ? 1u : 0u);
+        }
+        umma_bf16_ss(tmem + col, sdesc_aug(base + Lay::OFF_ONE),
+                     sdesc_aug(base + off_aug + st * kAugBytes), IDESC_S, 1u);
+      };
+      // D[col] += P^T or dS^T (A, tensor memory: 32 columns of each half of
+      // the queries) * step's rows (B)
+      auto issue_grad = [&](uint32_t col, uint32_t a, int off, int st, bool first) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_bf16_ts(tmem + col, tmem + a + (kk >> 2) * 64 + (kk & 3) * 8,
+                       sdesc_sw128(base + off + st * Lay::TILE_BYTES + kk * (16 * 128),
+                                   kTile * 128, 1024),
+                       IDESC_G, (!first || kk > 0) ? 1u : 0u);
+      };
+      bool ok = mbar_wait(kv_full, 0, wc) && mbar_wait(&q_full[0], 0, wc);
+      if (ok) {
+        tc_fence_after();
+        issue_scores(C_S, Lay::OFF_K, Lay::OFF_Q, Lay::OFF_QA, 0);
+        umma_commit(s_full);
+        ok = mbar_wait(&do_full[0], 0, wc);
+      }
+      if (ok) {
+        tc_fence_after();
+        issue_scores(C_DP, Lay::OFF_V, Lay::OFF_DO, Lay::OFF_DA, 0);
+        umma_commit(dp_full);
+      }
+      for (int j = 0; ok && j < n_it; ++j) {
+        const int st = j % NS, nx = (j + 1) % NS;
+        const uint32_t nx_parity = ((j + 1) / NS) & 1;
+        if (!(ok = mbar_wait(p_full, j & 1, wc))) break;
+        tc_fence_after();
+        issue_grad(C_DV, C_S, Lay::OFF_DO, st, j == 0);
+        umma_commit(&do_empty[st]);
+        if (j + 1 < n_it) {
+          if (!(ok = mbar_wait(&q_full[nx], nx_parity, wc))) break;
+          tc_fence_after();
+          issue_scores(C_S, Lay::OFF_K, Lay::OFF_Q, Lay::OFF_QA, nx);
+          umma_commit(s_full);
+        }
+        if (!(ok = mbar_wait(ds_full, j & 1, wc))) break;
+        tc_fence_after();
+        issue_grad(C_DK, C_DP, Lay::OFF_Q, st, j == 0);
+        umma_commit(&q_empty[st]);
+        if (j + 1 < n_it) {
+          if (!(ok = mbar_wait(&do_full[nx], nx_parity, wc))) break;
+          tc_fence_after();
+          issue_scores(C_DP, Lay::OFF_V, Lay::OFF_DO, Lay::OFF_DA, nx);
+          umma_commit(dp_full);
+        }
+      }
+      if (ok) {
+        umma_commit(acc_full);
+      } else {
+        umma_commit(drain_bar);
+        mbar_wait_drain(drain_bar, 0);
+      }
+    }
+  } else if (warp < 8) {
+    // ================================================================ scores
+    const int wl = warp & 3, half = warp >> 2;
+    const int r = wl * 32 + lane;        // key row within the tile, TMEM lane
+    const uint32_t at = tmem + (uint32_t(wl * 32) << 16);
+    const uint32_t s_col = at + C_S + 64 * half, dp_col = at + C_DP + 64 * half;
+    const int kb = (wl * 32) / BLK;      // key block within the tile (warp-uniform)
+    bool ok = true;
+    // The two 32-column groups' entries of step j + 1 are fetched in step j.
+    const int slot[2] = {(64 * half) / BLK, (64 * half + 32) / BLK};
+    int ent[2], next[2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) next[g] = slot[g] < n_ent ? __ldg(p.entry + e0 + slot[g]) : 0;
+    for (int j = 0; j < n_it; ++j) {
+      bool on[2];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        ent[g] = next[g];
+        const int idx = (j + 1) * EPI + slot[g];
+        next[g] = idx < n_ent ? __ldg(p.entry + e0 + idx) : 0;
+        on[g] = ((ent[g] >> 16) >> kb) & 1;
+      }
+      if (!(ok = warp_wait(s_full, j & 1, wc))) break;
+      tc_fence_after();
+      float w[64];
+      float (&w0)[32] = *reinterpret_cast<float(*)[32]>(&w[0]);
+      float (&w1)[32] = *reinterpret_cast<float(*)[32]>(&w[32]);
+      tmem_ld_64(s_col, w);
+      tmem_ld_wait();
+      // A group whose query block does not keep this key block has weight 0.
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        float (&x)[32] = g ? w1 : w0;
+        if (on[g]) {
+          exp2_scaled(x, p.scale_log2);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = 0.f;
+        }
+        tmem_st_bf16(s_col + 16 * g, x);
+      }
+      tmem_st_wait();
+      warp_arrive(p_full, lane);
+      if (!(ok = warp_wait(dp_full, j & 1, wc))) break;
+      tc_fence_after();
+      float y[64];
+      tmem_ld_64(dp_col, y);
+      tmem_ld_wait();
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        float (&x)[32] = *reinterpret_cast<float(*)[32]>(&y[32 * g]);
+        if (on[g]) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            f2_split(f2_mul(f2_make(x[i], x[i + 1]),
+                            f2_make(w[32 * g + i], w[32 * g + i + 1])), x[i], x[i + 1]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = 0.f;
+        }
+        tmem_st_bf16(dp_col + 16 * g, x);
+      }
+      tmem_st_wait();
+      warp_arrive(ds_full, lane);
+    }
+    // ---- results: warps 0-3 dV, warps 4-7 dK; rows of the padding are 0
+    const int row = kt * kTile + r;
+    const size_t out_at = (size_t(bh) * p.L_pad + row) * D;
+    void* out = half ? p.out1 : p.out0;
+    if (n_it > 0 && ok && (ok = warp_wait(acc_full, 0, wc))) {
+      tc_fence_after();
+      const float f = half ? p.scale : 1.f;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        float x[32];
+        tmem_ld32(at + (half ? C_DK : C_DV) + 32 * c, x);
+        tmem_ld_wait();
+        if (row < p.L)
+          store_row32<kOutBf16>(out, out_at + 32 * c, x, f);
+        else if (row < p.L_pad)
+          store_zero32<kOutBf16>(out, out_at + 32 * c);
+      }
+    } else if (n_it == 0 && row < p.L_pad) {
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) store_zero32<kOutBf16>(out, out_at + 32 * c);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ dQ
+
+template <int D> struct QueryLayout {
+  static constexpr int NS = D == 128 ? 3 : 4;  // stages of K and of V
+  static constexpr int TILE_BYTES = kTile * D * 2;
+  static constexpr int OFF_K = 0;
+  static constexpr int OFF_V = OFF_K + NS * TILE_BYTES;
+  static constexpr int OFF_BAR = OFF_V + NS * TILE_BYTES;
+  static constexpr int N_BARS = 4 * NS + 8;
+  static constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
+  static constexpr int BYTES = OFF_MISC + 16;
+  static constexpr int SMEM_ALLOC = BYTES + 1024;  // one CTA per SM, as above
+  static_assert(SMEM_ALLOC > 116 * 1024 && SMEM_ALLOC <= 227 * 1024, "shared memory");
+};
+
+// The CTA's own Q and dO rows are the A operands of every S and dP: they stay
+// in tensor memory (64 columns each at D = 128), which halves what those
+// products read from shared memory. Per step j the MMA thread issues S(j+1)
+// as soon as the softmax has S(j) in registers, then dQ(j) and dP(j+1); dS
+// takes dP's place as the A operand of dQ += dS K.
+template <int D, int BLK, bool kOutBf16>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    bwd_query_kernel(const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const BwdParams p) {
+  using Lay = QueryLayout<D>;
+  constexpr int NS = Lay::NS;
+  constexpr int EPI = kTile / BLK;
+  constexpr int SLABS = D / 64;
+  constexpr uint32_t C_S = 0, C_DP = 128, C_DQ = 256, C_Q = 256 + D, C_DO = C_Q + D / 2;
+  constexpr uint32_t IDESC_S = idesc_bf16_f32(kTile, kTile, false, false);
+  constexpr uint32_t IDESC_G = idesc_bf16_f32(kTile, D, false, true);
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::OFF_BAR);
+  uint64_t* k_full = bars;            // [NS]
+  uint64_t* k_empty = k_full + NS;    // [NS]
+  uint64_t* v_full = k_empty + NS;    // [NS]
+  uint64_t* v_empty = v_full + NS;    // [NS]
+  uint64_t* own_full = v_empty + NS;  // Q and dO in tensor memory
+  uint64_t* s_full = own_full + 1;
+  uint64_t* s_free = s_full + 1;
+  uint64_t* dp_full = s_free + 1;
+  uint64_t* ds_full = dp_full + 1;
+  uint64_t* acc_full = ds_full + 1;
+  uint64_t* drain_bar = acc_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::OFF_MISC + 4);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int tile = p.order[blockIdx.x];
+  const int bh = tile / p.n_qt;
+  const int qt = tile - bh * p.n_qt;
+  const int e0 = p.ptr[tile];
+  const int n_ent = p.ptr[tile + 1] - e0;  // at least 1: every query block keeps one
+  const int n_it = (n_ent + EPI - 1) / EPI;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    mbar_init(own_full, 8);
+    mbar_init(s_full, 1);
+    mbar_init(s_free, 8);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_full, 8);
+    mbar_init(acc_full, 1);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtx wc{abort_flag, p.status, p.wait_limit};
+
+  if (warp == 8) {
+    // ================================================================ producer
+    if (lane == 0) {
+      tma_prefetch_map(&tm_k);
+      tma_prefetch_map(&tm_v);
+      bool ok = true;
+      int loaded_k = 0, loaded_v = 0;
+      for (int j = 0; ok && j < n_it; ++j) {
+        const int st = j % NS;
+        const uint32_t parity = ((j / NS) & 1) ^ 1;
+        int row[EPI];
+#pragma unroll
+        for (int e = 0; e < EPI; ++e)
+          row[e] = (p.entry[e0 + min(j * EPI + e, n_ent - 1)] & 0xFFFF) * BLK;
+        auto load = [&](const CUtensorMap* map, uint64_t* full, int off) {
+          mbar_arrive_expect_tx(full, Lay::TILE_BYTES);
+#pragma unroll
+          for (int e = 0; e < EPI; ++e)
+#pragma unroll
+            for (int s = 0; s < SLABS; ++s)
+              tma_load_3d(smem + off + st * Lay::TILE_BYTES + s * (kTile * 128) + e * (BLK * 128),
+                          map, full, s * 64, row[e], bh);
+        };
+        if (!(ok = mbar_wait(&k_empty[st], parity, wc))) break;
+        load(&tm_k, &k_full[st], Lay::OFF_K);
+        ++loaded_k;
+        if (!(ok = mbar_wait(&v_empty[st], parity, wc))) break;
+        load(&tm_v, &v_full[st], Lay::OFF_V);
+        ++loaded_v;
+      }
+      if (!ok) {
+        for (int i = max(loaded_k - NS, 0); i < loaded_k; ++i)
+          mbar_wait_drain(&k_full[i % NS], (i / NS) & 1);
+        for (int i = max(loaded_v - NS, 0); i < loaded_v; ++i)
+          mbar_wait_drain(&v_full[i % NS], (i / NS) & 1);
+      }
+    }
+  } else if (warp == 9) {
+    // ================================================================ MMA issuer
+    if (lane == 0) {
+      const uint32_t base = smem_addr(smem);
+      auto issue_scores = [&](uint32_t col, uint32_t own, int off, int st) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_bf16_ts(tmem + col, tmem + own + kk * 8,
+                       sdesc_sw128(base + off + st * Lay::TILE_BYTES + (kk >> 2) * (kTile * 128) +
+                                       (kk & 3) * 32, 16, 1024),
+                       IDESC_S, kk > 0 ? 1u : 0u);
+      };
+      bool ok = mbar_wait(own_full, 0, wc) && mbar_wait(&k_full[0], 0, wc);
+      if (ok) {
+        tc_fence_after();
+        issue_scores(C_S, C_Q, Lay::OFF_K, 0);
+        umma_commit(s_full);
+        ok = mbar_wait(&v_full[0], 0, wc);
+      }
+      if (ok) {
+        tc_fence_after();
+        issue_scores(C_DP, C_DO, Lay::OFF_V, 0);
+        umma_commit(dp_full);
+        umma_commit(&v_empty[0]);
+      }
+      for (int j = 0; ok && j < n_it; ++j) {
+        const int st = j % NS, nx = (j + 1) % NS;
+        const uint32_t nx_parity = ((j + 1) / NS) & 1;
+        if (j + 1 < n_it) {
+          if (!(ok = mbar_wait(&k_full[nx], nx_parity, wc) && mbar_wait(s_free, j & 1, wc))) break;
+          tc_fence_after();
+          issue_scores(C_S, C_Q, Lay::OFF_K, nx);
+          umma_commit(s_full);
+        }
+        if (!(ok = mbar_wait(ds_full, j & 1, wc))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_bf16_ts(tmem + C_DQ, tmem + C_DP + (kk >> 2) * 64 + (kk & 3) * 8,
+                       sdesc_sw128(base + Lay::OFF_K + st * Lay::TILE_BYTES + kk * (16 * 128),
+                                   kTile * 128, 1024),
+                       IDESC_G, (j > 0 || kk > 0) ? 1u : 0u);
+        umma_commit(&k_empty[st]);
+        if (j + 1 < n_it) {
+          if (!(ok = mbar_wait(&v_full[nx], nx_parity, wc))) break;
+          tc_fence_after();
+          issue_scores(C_DP, C_DO, Lay::OFF_V, nx);
+          umma_commit(dp_full);
+          umma_commit(&v_empty[nx]);
+        }
+      }
+      if (ok) {
+        umma_commit(acc_full);
+      } else {
+        umma_commit(drain_bar);
+        mbar_wait_drain(drain_bar, 0);
+      }
+    }
+  } else if (warp < 8) {
+    // ================================================================ scores
+    const int wl = warp & 3, half = warp >> 2;
+    const int r = wl * 32 + lane;
+    const int row = qt * kTile + r;
+    const bool valid = row < p.L;
+    const size_t flat = size_t(bh) * p.L_pad + row;
+    const uint32_t at = tmem + (uint32_t(wl * 32) << 16);
+    const uint32_t s_col = at + C_S + 64 * half, dp_col = at + C_DP + 64 * half;
+    const int qb = (wl * 32) / BLK;
+    // Own rows to tensor memory: warps 0-3 Q, warps 4-7 dO; zero past L.
+    {
+      const uint16_t* src = static_cast<const uint16_t*>(half ? p.d_o : p.q) + flat * D;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t u[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (valid) x = __ldg(reinterpret_cast<const uint4*>(src + c * 32 + i * 8));
+          u[4 * i] = x.x, u[4 * i + 1] = x.y, u[4 * i + 2] = x.z, u[4 * i + 3] = x.w;
+        }
+        tmem_st16(at + (half ? C_DO : C_Q) + 16 * c, u);
+      }
+      tmem_st_wait();
+      warp_arrive(own_full, lane);
+    }
+    const float NEG_INF = -__int_as_float(0x7f800000);
+    const float shift = valid ? -p.lse[flat] * 1.4426950408889634f : NEG_INF;
+    const float delta = valid ? p.delta[flat] : 0.f;
+    bool ok = true;
+    const int slot[2] = {(64 * half) / BLK, (64 * half + 32) / BLK};
+    int ent[2], next[2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) next[g] = slot[g] < n_ent ? __ldg(p.entry + e0 + slot[g]) : 0;
+    for (int j = 0; j < n_it; ++j) {
+      bool on[2];
+      int lim[2];  // valid columns of the group
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        ent[g] = next[g];
+        const int idx = (j + 1) * EPI + slot[g];
+        next[g] = idx < n_ent ? __ldg(p.entry + e0 + idx) : 0;
+        lim[g] = p.L - (ent[g] & 0xFFFF) * BLK - (64 * half + 32 * g) % BLK;
+        on[g] = (((ent[g] >> 16) >> qb) & 1) && lim[g] > 0;
+      }
+      if (!(ok = warp_wait(s_full, j & 1, wc))) break;
+      tc_fence_after();
+      float w[64];
+      tmem_ld_64(s_col, w);
+      tmem_ld_wait();
+      warp_arrive(s_free, lane);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        float (&x)[32] = *reinterpret_cast<float(*)[32]>(&w[32 * g]);
+        if (!on[g]) continue;
+        exp2_shifted(x, p.scale_log2, shift);
+      }
+      if (!(ok = warp_wait(dp_full, j & 1, wc))) break;
+      tc_fence_after();
+      float y[64];
+      tmem_ld_64(dp_col, y);
+      tmem_ld_wait();
+      const f32x2 nd = f2_make(-delta, -delta);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        float (&x)[32] = *reinterpret_cast<float(*)[32]>(&y[32 * g]);
+        if (on[g]) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            f2_split(f2_mul(f2_add(f2_make(x[i], x[i + 1]), nd),
+                            f2_make(w[32 * g + i], w[32 * g + i + 1])), x[i], x[i + 1]);
+          if (lim[g] < 32) {
+            // Keys of the padding score 0, whose weight can overflow.
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i >= lim[g]) x[i] = 0.f;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = 0.f;
+        }
+        tmem_st_bf16(dp_col + 16 * g, x);
+      }
+      tmem_st_wait();
+      warp_arrive(ds_full, lane);
+    }
+    if (ok && (ok = warp_wait(acc_full, 0, wc))) {
+      tc_fence_after();
+      // The two halves of the columns; rows of the padding are 0.
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        float x[32];
+        const int col = half * (D / 2) + 32 * c;
+        tmem_ld32(at + C_DQ + col, x);
+        tmem_ld_wait();
+        if (valid)
+          store_row32<kOutBf16>(p.out0, flat * D + col, x, p.scale);
+        else if (row < p.L_pad)
+          store_zero32<kOutBf16>(p.out0, flat * D + col);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, int BLK, bool kOutBf16>
+cudaError_t run_mma(const BackwardCall& c, const BackwardOperands& w, BwdParams p,
+                    cudaStream_t stream) {
+  const losa_pattern* pat = c.p;
+  const int BH = pat->B * pat->H;
+  constexpr int box = BLK;
+  CUtensorMap k_own, v_own, q_step, do_step, k_step, v_step;
+  // Rows past L read as zero, whatever they hold.
+  if (!make_slab_map(&k_own, c.k, BH, c.L, p.L_pad, D, kTile, 2, false) ||
+      !make_slab_map(&v_own, c.v, BH, c.L, p.L_pad, D, kTile, 2, false) ||
+      !make_slab_map(&q_step, c.q, BH, c.L, p.L_pad, D, box, 2, false) ||
+      !make_slab_map(&do_step, w.d_o, BH, c.L, p.L_pad, D, box, 2, false) ||
+      !make_slab_map(&k_step, c.k, BH, c.L, p.L_pad, D, box, 2, false) ||
+      !make_slab_map(&v_step, c.v, BH, c.L, p.L_pad, D, box, 2, false))
+    return cudaErrorInvalidValue;
+  auto keys = bwd_key_kernel<D, BLK, kOutBf16>;
+  auto queries = bwd_query_kernel<D, BLK, kOutBf16>;
+  cudaError_t err = cudaFuncSetAttribute(keys, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         KeyLayout<D>::SMEM_ALLOC);
+  if (err != cudaSuccess) return err;
+  err = cudaFuncSetAttribute(queries, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             QueryLayout<D>::SMEM_ALLOC);
+  if (err != cudaSuccess) return err;
+  p.ptr = pat->key_ptr;
+  p.entry = pat->key_entry;
+  p.order = pat->key_order;
+  p.out0 = c.dv;
+  p.out1 = c.dk;
+  keys<<<unsigned(pat->n_tiles), kBwdThreads, KeyLayout<D>::SMEM_ALLOC, stream>>>(
+      k_own, v_own, q_step, do_step, p);
+  err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  p.ptr = pat->tile_ptr;
+  p.entry = pat->tile_entry;
+  p.order = pat->tile_order;
+  p.out0 = c.dq;
+  p.out1 = nullptr;
+  queries<<<unsigned(pat->n_tiles), kBwdThreads, QueryLayout<D>::SMEM_ALLOC, stream>>>(
+      k_step, v_step, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_backward_mma(const BackwardCall& c, const BackwardOperands& w,
+                                cudaStream_t stream) {
+  const losa_pattern* pat = c.p;
+  BwdParams p{};
+  p.L = c.L;
+  p.L_pad = pat->n_blocks * pat->block;
+  p.n_qt = pat->n_qt;
+  p.n_tiles = int(pat->n_tiles);
+  p.scale = c.scale;
+  p.scale_log2 = c.scale * 1.4426950408889634f;
+  p.lse = c.lse;
+  p.delta = w.delta;
+  p.q_aug = w.q_aug;
+  p.do_aug = w.do_aug;
+  p.q = c.q;
+  p.d_o = w.d_o;
+  p.status = device_status_word();
+  if (!p.status) return cudaErrorInvalidDevice;
+  p.wait_limit = wait_limit();
+#define LOSA_BWD_CASE(D_, BLK_)                                       \
+  if (c.d == D_ && pat->block == BLK_)                                \
+    return c.out_bf16 ? run_mma<D_, BLK_, true>(c, w, p, stream)      \
+                      : run_mma<D_, BLK_, false>(c, w, p, stream);
+  LOSA_BWD_CASE(128, 128)
+  LOSA_BWD_CASE(128, 64)
+  LOSA_BWD_CASE(128, 32)
+  LOSA_BWD_CASE(64, 128)
+  LOSA_BWD_CASE(64, 64)
+  LOSA_BWD_CASE(64, 32)
+#undef LOSA_BWD_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace losa

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 
@@ -90,6 +91,11 @@ cudaError_t launch_sparse(const void* q, const void* k, const void* v, bool tf32
 // Wait limit (SM cycles) of the attention kernels launched after the call;
 // 0 restores the default.
 void set_wait_limit(long long cycles);
+long long wait_limit();
+
+// TMA map of a [BH, L_pad, d] tensor in 128-byte-wide slabs (losa_attention.cu).
+bool make_slab_map(CUtensorMap* map, const void* base, int BH, int rows, int L_pad, int d,
+                   int box_rows, int esz, bool atom32);
 
 // One bounded mbarrier wait that must run out (diagnostic).
 cudaError_t launch_wait_selftest(long long limit_cycles, cudaStream_t stream);
@@ -163,6 +169,17 @@ struct BackwardCall {
 };
 size_t backward_workspace(const losa_pattern* p, int d, bool in_bf16, bool do_bf16);
 cudaError_t launch_backward(const BackwardCall& c, cudaStream_t stream);
+
+// The bf16 path's kernels (losa_backward_mma.cu): d_o is bf16, delta D, and
+// q_aug, do_aug the rows that carry lse and D into the products (both as the
+// prepass leaves them).
+struct BackwardOperands {
+  const void* d_o;
+  const float* delta;
+  const uint16_t *q_aug, *do_aug;
+};
+cudaError_t launch_backward_mma(const BackwardCall& c, const BackwardOperands& w,
+                                cudaStream_t stream);
 
 // One call of losa_rope_pack (unpack false) or losa_rope_unpack, validated
 // by the caller; strides belong to the token-major side.
