@@ -36,12 +36,49 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// Matrix descriptor of a K-major operand of 16 bf16 columns without swizzle:
-// 8-row groups of 256 bytes (SBO), each two 8 x 16-byte core matrices 128
-// bytes apart (LBO).
-__device__ __forceinline__ uint64_t sdesc_aug(uint32_t saddr) {
-  return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(128 >> 4) << 16) |
-         (uint64_t(256 >> 4) << 32) | (1ull << 46);
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(yes));
+  return yes != 0;
+}
+
+// Shared-memory matrix descriptors in two halves. The low one is the start
+// address and the stride LBO, both in units of 16 bytes; a shared-memory
+// address needs 14 bits in those units, so a step along an operand is an
+// addition to it. The high half is a constant per layout: SBO, the
+// descriptor's version (bit 46) and the swizzle (bits 61 to 63).
+__device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+  return (saddr >> 4) | ((lbo_bytes >> 4) << 16);
+}
+// Rows of 128 bytes, 128-byte swizzle, 8-row groups 1 KB apart (K-major with
+// any LBO, MN-major with LBO the distance of 64-column slabs).
+constexpr uint32_t kDescSw128 = (1024u >> 4) | (1u << 14) | (2u << 29);
+// K-major operand of 16 bf16 columns without swizzle: 8-row groups of 256
+// bytes (SBO), each two 8 x 16-byte core matrices 128 bytes apart (LBO).
+constexpr uint32_t kDescAug = (256u >> 4) | (1u << 14);
+
+template <uint32_t kHiA, uint32_t kHiB>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %6};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kHiA), "n"(kHiB)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tmov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescSw128)
+      : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld_64(uint32_t taddr, float (&r)[64]) {
@@ -299,72 +336,77 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   } else if (warp == 9) {
     // ================================================================ MMA issuer
-    if (lane == 0 && n_it > 0) {
+    // The whole warp walks the loop and one elected lane issues, so that the
+    // descriptors are warp-uniform values (issued from a branch of one lane,
+    // an MMA instruction took about 100 cycles instead of its 64).
+    if (n_it > 0) {
       const uint32_t base = smem_addr(smem);
+      const uint32_t one_lo = sdesc_lo(base + Lay::OFF_ONE, 128);
       // D[col] = own (A) * step's rows (B)^T + ones * aug^T
-      auto issue_scores = [&](uint32_t col, int own, int off, int off_aug, int st) {
+      auto issue_scores = [&](uint32_t col, int own, int off, int off_aug, int st,
+                              uint64_t* done) {
+        const uint32_t a = sdesc_lo(base + own, 16);
+        const uint32_t b = sdesc_lo(base + off + st * Lay::TILE_BYTES, 16);
+        const uint32_t g = sdesc_lo(base + off_aug + st * kAugBytes, 128);
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t o = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
-          umma_bf16_ss(tmem + col, sdesc_sw128(base + own + o, 16, 1024),
-                       sdesc_sw128(base + off + st * Lay::TILE_BYTES + o, 16, 1024), IDESC_S,
-                       kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
+            mma_ss<kDescSw128, kDescSw128>(tmem + col, a + o, b + o, IDESC_S, kk > 0 ? 1u : 0u);
+          }
+          mma_ss<kDescAug, kDescAug>(tmem + col, one_lo, g, IDESC_S, 1u);
+          umma_commit(done);
         }
-        umma_bf16_ss(tmem + col, sdesc_aug(base + Lay::OFF_ONE),
-                     sdesc_aug(base + off_aug + st * kAugBytes), IDESC_S, 1u);
+        __syncwarp();
       };
       // D[col] += P^T or dS^T (A, tensor memory: 32 columns of each half of
       // the queries) * step's rows (B)
-      auto issue_grad = [&](uint32_t col, uint32_t a, int off, int st, bool first) {
+      auto issue_grad = [&](uint32_t col, uint32_t a, int off, int st, bool first,
+                            uint64_t* done) {
+        const uint32_t b = sdesc_lo(base + off + st * Lay::TILE_BYTES, kTile * 128);
+        const uint32_t acc = first ? 0u : 1u;
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_bf16_ts(tmem + col, tmem + a + (kk >> 2) * 64 + (kk & 3) * 8,
-                       sdesc_sw128(base + off + st * Lay::TILE_BYTES + kk * (16 * 128),
-                                   kTile * 128, 1024),
-                       IDESC_G, (!first || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(tmem + col, tmem + a + (kk >> 2) * 64 + (kk & 3) * 8,
+                   b + ((kk * 16 * 128) >> 4), IDESC_G, kk > 0 ? 1u : acc);
+          umma_commit(done);
+        }
+        __syncwarp();
       };
-      bool ok = mbar_wait(kv_full, 0, wc) && mbar_wait(&q_full[0], 0, wc);
+      bool ok = warp_wait(kv_full, 0, wc) && warp_wait(&q_full[0], 0, wc);
       if (ok) {
         tc_fence_after();
-        issue_scores(C_S, Lay::OFF_K, Lay::OFF_Q, Lay::OFF_QA, 0);
-        umma_commit(s_full);
-        ok = mbar_wait(&do_full[0], 0, wc);
+        issue_scores(C_S, Lay::OFF_K, Lay::OFF_Q, Lay::OFF_QA, 0, s_full);
+        ok = warp_wait(&do_full[0], 0, wc);
       }
       if (ok) {
         tc_fence_after();
-        issue_scores(C_DP, Lay::OFF_V, Lay::OFF_DO, Lay::OFF_DA, 0);
-        umma_commit(dp_full);
+        issue_scores(C_DP, Lay::OFF_V, Lay::OFF_DO, Lay::OFF_DA, 0, dp_full);
       }
       for (int j = 0; ok && j < n_it; ++j) {
         const int st = j % NS, nx = (j + 1) % NS;
         const uint32_t nx_parity = ((j + 1) / NS) & 1;
-        if (!(ok = mbar_wait(p_full, j & 1, wc))) break;
+        if (!(ok = warp_wait(p_full, j & 1, wc))) break;
         tc_fence_after();
-        issue_grad(C_DV, C_S, Lay::OFF_DO, st, j == 0);
-        umma_commit(&do_empty[st]);
+        issue_grad(C_DV, C_S, Lay::OFF_DO, st, j == 0, &do_empty[st]);
         if (j + 1 < n_it) {
-          if (!(ok = mbar_wait(&q_full[nx], nx_parity, wc))) break;
+          if (!(ok = warp_wait(&q_full[nx], nx_parity, wc))) break;
           tc_fence_after();
-          issue_scores(C_S, Lay::OFF_K, Lay::OFF_Q, Lay::OFF_QA, nx);
-          umma_commit(s_full);
+          issue_scores(C_S, Lay::OFF_K, Lay::OFF_Q, Lay::OFF_QA, nx, s_full);
         }
-        if (!(ok = mbar_wait(ds_full, j & 1, wc))) break;
+        if (!(ok = warp_wait(ds_full, j & 1, wc))) break;
         tc_fence_after();
-        issue_grad(C_DK, C_DP, Lay::OFF_Q, st, j == 0);
-        umma_commit(&q_empty[st]);
+        issue_grad(C_DK, C_DP, Lay::OFF_Q, st, j == 0, &q_empty[st]);
         if (j + 1 < n_it) {
-          if (!(ok = mbar_wait(&do_full[nx], nx_parity, wc))) break;
+          if (!(ok = warp_wait(&do_full[nx], nx_parity, wc))) break;
           tc_fence_after();
-          issue_scores(C_DP, Lay::OFF_V, Lay::OFF_DO, Lay::OFF_DA, nx);
-          umma_commit(dp_full);
+          issue_scores(C_DP, Lay::OFF_V, Lay::OFF_DO, Lay::OFF_DA, nx, dp_full);
         }
       }
-      if (ok) {
-        umma_commit(acc_full);
-      } else {
-        umma_commit(drain_bar);
-        mbar_wait_drain(drain_bar, 0);
-      }
+      // The end of the MMAs: for the results, or (aborted) before TMEM is freed.
+      if (elect_one()) umma_commit(ok ? acc_full : drain_bar);
+      if (!ok) mbar_wait_drain(drain_bar, 0);
     }
   } else if (warp < 8) {
     // ================================================================ scores
@@ -585,62 +627,61 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   } else if (warp == 9) {
     // ================================================================ MMA issuer
-    if (lane == 0) {
-      const uint32_t base = smem_addr(smem);
-      auto issue_scores = [&](uint32_t col, uint32_t own, int off, int st) {
+    const uint32_t base = smem_addr(smem);
+    auto issue_scores = [&](uint32_t col, uint32_t own, int off, int st, uint64_t* done,
+                            uint64_t* free) {
+      const uint32_t b = sdesc_lo(base + off + st * Lay::TILE_BYTES, 16);
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          umma_bf16_ts(tmem + col, tmem + own + kk * 8,
-                       sdesc_sw128(base + off + st * Lay::TILE_BYTES + (kk >> 2) * (kTile * 128) +
-                                       (kk & 3) * 32, 16, 1024),
-                       IDESC_S, kk > 0 ? 1u : 0u);
-      };
-      bool ok = mbar_wait(own_full, 0, wc) && mbar_wait(&k_full[0], 0, wc);
-      if (ok) {
-        tc_fence_after();
-        issue_scores(C_S, C_Q, Lay::OFF_K, 0);
-        umma_commit(s_full);
-        ok = mbar_wait(&v_full[0], 0, wc);
+          mma_ts(tmem + col, tmem + own + kk * 8,
+                 b + (((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4), IDESC_S,
+                 kk > 0 ? 1u : 0u);
+        umma_commit(done);
+        if (free) umma_commit(free);
       }
-      if (ok) {
+      __syncwarp();
+    };
+    bool ok = warp_wait(own_full, 0, wc) && warp_wait(&k_full[0], 0, wc);
+    if (ok) {
+      tc_fence_after();
+      issue_scores(C_S, C_Q, Lay::OFF_K, 0, s_full, nullptr);
+      ok = warp_wait(&v_full[0], 0, wc);
+    }
+    if (ok) {
+      tc_fence_after();
+      issue_scores(C_DP, C_DO, Lay::OFF_V, 0, dp_full, &v_empty[0]);
+    }
+    for (int j = 0; ok && j < n_it; ++j) {
+      const int st = j % NS, nx = (j + 1) % NS;
+      const uint32_t nx_parity = ((j + 1) / NS) & 1;
+      if (j + 1 < n_it) {
+        if (!(ok = warp_wait(&k_full[nx], nx_parity, wc) && warp_wait(s_free, j & 1, wc))) break;
         tc_fence_after();
-        issue_scores(C_DP, C_DO, Lay::OFF_V, 0);
-        umma_commit(dp_full);
-        umma_commit(&v_empty[0]);
+        issue_scores(C_S, C_Q, Lay::OFF_K, nx, s_full, nullptr);
       }
-      for (int j = 0; ok && j < n_it; ++j) {
-        const int st = j % NS, nx = (j + 1) % NS;
-        const uint32_t nx_parity = ((j + 1) / NS) & 1;
-        if (j + 1 < n_it) {
-          if (!(ok = mbar_wait(&k_full[nx], nx_parity, wc) && mbar_wait(s_free, j & 1, wc))) break;
-          tc_fence_after();
-          issue_scores(C_S, C_Q, Lay::OFF_K, nx);
-          umma_commit(s_full);
-        }
-        if (!(ok = mbar_wait(ds_full, j & 1, wc))) break;
-        tc_fence_after();
+      if (!(ok = warp_wait(ds_full, j & 1, wc))) break;
+      tc_fence_after();
+      {
+        const uint32_t b = sdesc_lo(base + Lay::OFF_K + st * Lay::TILE_BYTES, kTile * 128);
+        const uint32_t acc = j > 0 ? 1u : 0u;
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_bf16_ts(tmem + C_DQ, tmem + C_DP + (kk >> 2) * 64 + (kk & 3) * 8,
-                       sdesc_sw128(base + Lay::OFF_K + st * Lay::TILE_BYTES + kk * (16 * 128),
-                                   kTile * 128, 1024),
-                       IDESC_G, (j > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(&k_empty[st]);
-        if (j + 1 < n_it) {
-          if (!(ok = mbar_wait(&v_full[nx], nx_parity, wc))) break;
-          tc_fence_after();
-          issue_scores(C_DP, C_DO, Lay::OFF_V, nx);
-          umma_commit(dp_full);
-          umma_commit(&v_empty[nx]);
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(tmem + C_DQ, tmem + C_DP + (kk >> 2) * 64 + (kk & 3) * 8,
+                   b + ((kk * 16 * 128) >> 4), IDESC_G, kk > 0 ? 1u : acc);
+          umma_commit(&k_empty[st]);
         }
+        __syncwarp();
       }
-      if (ok) {
-        umma_commit(acc_full);
-      } else {
-        umma_commit(drain_bar);
-        mbar_wait_drain(drain_bar, 0);
+      if (j + 1 < n_it) {
+        if (!(ok = warp_wait(&v_full[nx], nx_parity, wc))) break;
+        tc_fence_after();
+        issue_scores(C_DP, C_DO, Lay::OFF_V, nx, dp_full, &v_empty[nx]);
       }
     }
+    if (elect_one()) umma_commit(ok ? acc_full : drain_bar);
+    if (!ok) mbar_wait_drain(drain_bar, 0);
   } else if (warp < 8) {
     // ================================================================ scores
     const int wl = warp & 3, half = warp >> 2;
