@@ -11,6 +11,11 @@ namespace losa {
 namespace {
 
 constexpr int kBwdThreads = 384;
+// Launched with 168 registers a thread (checked at build time); the control
+// warpgroup gives some back to the two that hold scores.
+constexpr int kBwdLaunchRegs = 168, kScoreRegs = 216, kControlRegs = 72;
+static_assert(2 * 128 * kScoreRegs + 128 * kControlRegs == kBwdThreads * kBwdLaunchRegs,
+              "register split must use exactly the launch allocation");
 constexpr int kTile = 128;  // rows a CTA owns, and rows of a step
 constexpr int kAugBytes = kTile * 32;
 
@@ -81,9 +86,21 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld_64(uint32_t taddr, float (&r)[64]) {
-  tmem_ld32(taddr, *reinterpret_cast<float(*)[32]>(&r[0]));
-  tmem_ld32(taddr + 32, *reinterpret_cast<float(*)[32]>(&r[32]));
+__device__ __forceinline__ void zero32(float (&x)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) x[i] = 0.f;
+}
+__device__ __forceinline__ void mul32(float (&x)[32], const float (&w)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 2)
+    f2_split(f2_mul(f2_make(x[i], x[i + 1]), f2_make(w[i], w[i + 1])), x[i], x[i + 1]);
+}
+// x = (x + c) * w
+__device__ __forceinline__ void add_mul32(float (&x)[32], float c, const float (&w)[32]) {
+  const f32x2 c2 = f2_make(c, c);
+#pragma unroll
+  for (int i = 0; i < 32; i += 2)
+    f2_split(f2_mul(f2_add(f2_make(x[i], x[i + 1]), c2), f2_make(w[i], w[i + 1])), x[i], x[i + 1]);
 }
 
 // One arrival per warp: every lane's tensor-memory accesses are complete
@@ -234,8 +251,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   uint64_t* kv_full = do_empty + NS;   // K and V
   uint64_t* s_full = kv_full + 1;
   uint64_t* dp_full = s_full + 1;
-  uint64_t* p_full = dp_full + 1;
-  uint64_t* ds_full = p_full + 1;
+  uint64_t* p_full = dp_full + 1;  // [2] first, second 32 columns of each half
+  uint64_t* ds_full = p_full + 2;
   uint64_t* acc_full = ds_full + 1;
   uint64_t* drain_bar = acc_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::OFF_MISC);
@@ -260,7 +277,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     mbar_init(kv_full, 1);
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
-    mbar_init(p_full, 8);
+    mbar_init(&p_full[0], 8);
+    mbar_init(&p_full[1], 8);
     mbar_init(ds_full, 8);
     mbar_init(acc_full, 1);
     mbar_init(drain_bar, 1);
@@ -281,6 +299,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wc{abort_flag, p.status, p.wait_limit};
 
+  if (warp >= 8) {
+  reg_dealloc<kControlRegs>();
   if (warp == 8) {
     // ================================================================ producer
     if (lane == 0 && n_it > 0) {
@@ -360,17 +380,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         __syncwarp();
       };
       // D[col] += P^T or dS^T (A, tensor memory: 32 columns of each half of
-      // the queries) * step's rows (B)
-      auto issue_grad = [&](uint32_t col, uint32_t a, int off, int st, bool first,
+      // the queries) * step's rows (B), over the first (part 0) or second 32
+      // query rows of each half.
+      auto issue_grad = [&](uint32_t col, uint32_t a, int off, int st, int part, bool first,
                             uint64_t* done) {
-        const uint32_t b = sdesc_lo(base + off + st * Lay::TILE_BYTES, kTile * 128);
+        const uint32_t b = sdesc_lo(base + off + st * Lay::TILE_BYTES + part * (32 * 128),
+                                    kTile * 128);
+        const uint32_t at = tmem + a + part * 16;
         const uint32_t acc = first ? 0u : 1u;
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ts(tmem + col, tmem + a + (kk >> 2) * 64 + (kk & 3) * 8,
-                   b + ((kk * 16 * 128) >> 4), IDESC_G, kk > 0 ? 1u : acc);
-          umma_commit(done);
+          for (int i = 0; i < 4; ++i)
+            mma_ts(tmem + col, at + (i >> 1) * 64 + (i & 1) * 8,
+                   b + (((i >> 1) * 64 + (i & 1) * 16) * 128 >> 4), IDESC_G, i > 0 ? 1u : acc);
+          if (done) umma_commit(done);
         }
         __syncwarp();
       };
@@ -387,9 +410,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int j = 0; ok && j < n_it; ++j) {
         const int st = j % NS, nx = (j + 1) % NS;
         const uint32_t nx_parity = ((j + 1) / NS) & 1;
-        if (!(ok = warp_wait(p_full, j & 1, wc))) break;
+        if (!(ok = warp_wait(&p_full[0], j & 1, wc))) break;
         tc_fence_after();
-        issue_grad(C_DV, C_S, Lay::OFF_DO, st, j == 0, &do_empty[st]);
+        issue_grad(C_DV, C_S, Lay::OFF_DO, st, 0, j == 0, nullptr);
+        if (!(ok = warp_wait(&p_full[1], j & 1, wc))) break;
+        tc_fence_after();
+        issue_grad(C_DV, C_S, Lay::OFF_DO, st, 1, false, &do_empty[st]);
         if (j + 1 < n_it) {
           if (!(ok = warp_wait(&q_full[nx], nx_parity, wc))) break;
           tc_fence_after();
@@ -397,7 +423,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         if (!(ok = warp_wait(ds_full, j & 1, wc))) break;
         tc_fence_after();
-        issue_grad(C_DK, C_DP, Lay::OFF_Q, st, j == 0, &q_empty[st]);
+        issue_grad(C_DK, C_DP, Lay::OFF_Q, st, 0, j == 0, nullptr);
+        issue_grad(C_DK, C_DP, Lay::OFF_Q, st, 1, false, &q_empty[st]);
         if (j + 1 < n_it) {
           if (!(ok = warp_wait(&do_full[nx], nx_parity, wc))) break;
           tc_fence_after();
@@ -408,7 +435,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (elect_one()) umma_commit(ok ? acc_full : drain_bar);
       if (!ok) mbar_wait_drain(drain_bar, 0);
     }
-  } else if (warp < 8) {
+  }
+  } else {
+    reg_alloc<kScoreRegs>();
     // ================================================================ scores
     const int wl = warp & 3, half = warp >> 2;
     const int r = wl * 32 + lane;        // key row within the tile, TMEM lane
@@ -432,44 +461,47 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       if (!(ok = warp_wait(s_full, j & 1, wc))) break;
       tc_fence_after();
+      // Two groups of 32 columns, the second loaded and the first stored
+      // under the other's arithmetic; the first can feed dV at once. A group
+      // whose query block does not keep this key block has weight 0.
       float w[64];
       float (&w0)[32] = *reinterpret_cast<float(*)[32]>(&w[0]);
       float (&w1)[32] = *reinterpret_cast<float(*)[32]>(&w[32]);
-      tmem_ld_64(s_col, w);
+      tmem_ld32(s_col, w0);
       tmem_ld_wait();
-      // A group whose query block does not keep this key block has weight 0.
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        float (&x)[32] = g ? w1 : w0;
-        if (on[g]) {
-          exp2_scaled(x, p.scale_log2);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = 0.f;
-        }
-        tmem_st_bf16(s_col + 16 * g, x);
-      }
+      tmem_ld32(s_col + 32, w1);
+      if (on[0])
+        exp2_scaled(w0, p.scale_log2);
+      else
+        zero32(w0);
+      tmem_st_bf16(s_col, w0);
+      tmem_ld_wait();
       tmem_st_wait();
-      warp_arrive(p_full, lane);
+      warp_arrive(&p_full[0], lane);
+      if (on[1])
+        exp2_scaled(w1, p.scale_log2);
+      else
+        zero32(w1);
+      tmem_st_bf16(s_col + 16, w1);
+      tmem_st_wait();
+      warp_arrive(&p_full[1], lane);
       if (!(ok = warp_wait(dp_full, j & 1, wc))) break;
       tc_fence_after();
-      float y[64];
-      tmem_ld_64(dp_col, y);
+      float y0[32], y1[32];
+      tmem_ld32(dp_col, y0);
       tmem_ld_wait();
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        float (&x)[32] = *reinterpret_cast<float(*)[32]>(&y[32 * g]);
-        if (on[g]) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            f2_split(f2_mul(f2_make(x[i], x[i + 1]),
-                            f2_make(w[32 * g + i], w[32 * g + i + 1])), x[i], x[i + 1]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = 0.f;
-        }
-        tmem_st_bf16(dp_col + 16 * g, x);
-      }
+      tmem_ld32(dp_col + 32, y1);
+      if (on[0])
+        mul32(y0, w0);
+      else
+        zero32(y0);
+      tmem_st_bf16(dp_col, y0);
+      tmem_ld_wait();
+      if (on[1])
+        mul32(y1, w1);
+      else
+        zero32(y1);
+      tmem_st_bf16(dp_col + 16, y1);
       tmem_st_wait();
       warp_arrive(ds_full, lane);
     }
@@ -549,8 +581,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   uint64_t* s_full = own_full + 1;
   uint64_t* s_free = s_full + 1;
   uint64_t* dp_full = s_free + 1;
-  uint64_t* ds_full = dp_full + 1;
-  uint64_t* acc_full = ds_full + 1;
+  uint64_t* ds_full = dp_full + 1;  // [2] first, second 32 columns of each half
+  uint64_t* acc_full = ds_full + 2;
   uint64_t* drain_bar = acc_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::OFF_MISC + 4);
@@ -575,7 +607,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     mbar_init(s_full, 1);
     mbar_init(s_free, 8);
     mbar_init(dp_full, 1);
-    mbar_init(ds_full, 8);
+    mbar_init(&ds_full[0], 8);
+    mbar_init(&ds_full[1], 8);
     mbar_init(acc_full, 1);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -588,6 +621,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wc{abort_flag, p.status, p.wait_limit};
 
+  if (warp >= 8) {
+  reg_dealloc<kControlRegs>();
   if (warp == 8) {
     // ================================================================ producer
     if (lane == 0) {
@@ -642,6 +677,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       __syncwarp();
     };
+    // dQ += dS (A, tensor memory) * K_j (B), over the first (part 0) or second
+    // 32 keys of each half.
+    auto issue_grad = [&](int st, int part, bool first, uint64_t* done) {
+      const uint32_t b = sdesc_lo(base + Lay::OFF_K + st * Lay::TILE_BYTES + part * (32 * 128),
+                                  kTile * 128);
+      const uint32_t at = tmem + C_DP + part * 16;
+      const uint32_t acc = first ? 0u : 1u;
+      if (elect_one()) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          mma_ts(tmem + C_DQ, at + (i >> 1) * 64 + (i & 1) * 8,
+                 b + (((i >> 1) * 64 + (i & 1) * 16) * 128 >> 4), IDESC_G, i > 0 ? 1u : acc);
+        if (done) umma_commit(done);
+      }
+      __syncwarp();
+    };
     bool ok = warp_wait(own_full, 0, wc) && warp_wait(&k_full[0], 0, wc);
     if (ok) {
       tc_fence_after();
@@ -660,20 +711,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tc_fence_after();
         issue_scores(C_S, C_Q, Lay::OFF_K, nx, s_full, nullptr);
       }
-      if (!(ok = warp_wait(ds_full, j & 1, wc))) break;
+      if (!(ok = warp_wait(&ds_full[0], j & 1, wc))) break;
       tc_fence_after();
-      {
-        const uint32_t b = sdesc_lo(base + Lay::OFF_K + st * Lay::TILE_BYTES, kTile * 128);
-        const uint32_t acc = j > 0 ? 1u : 0u;
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ts(tmem + C_DQ, tmem + C_DP + (kk >> 2) * 64 + (kk & 3) * 8,
-                   b + ((kk * 16 * 128) >> 4), IDESC_G, kk > 0 ? 1u : acc);
-          umma_commit(&k_empty[st]);
-        }
-        __syncwarp();
-      }
+      issue_grad(st, 0, j == 0, nullptr);
+      if (!(ok = warp_wait(&ds_full[1], j & 1, wc))) break;
+      tc_fence_after();
+      issue_grad(st, 1, false, &k_empty[st]);
       if (j + 1 < n_it) {
         if (!(ok = warp_wait(&v_full[nx], nx_parity, wc))) break;
         tc_fence_after();
@@ -682,7 +725,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     if (elect_one()) umma_commit(ok ? acc_full : drain_bar);
     if (!ok) mbar_wait_drain(drain_bar, 0);
-  } else if (warp < 8) {
+  }
+  } else {
+    reg_alloc<kScoreRegs>();
     // ================================================================ scores
     const int wl = warp & 3, half = warp >> 2;
     const int r = wl * 32 + lane;
@@ -714,60 +759,70 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const float delta = valid ? p.delta[flat] : 0.f;
     bool ok = true;
     const int slot[2] = {(64 * half) / BLK, (64 * half + 32) / BLK};
-    int ent[2], next[2];
+    int next[2];
 #pragma unroll
     for (int g = 0; g < 2; ++g) next[g] = slot[g] < n_ent ? __ldg(p.entry + e0 + slot[g]) : 0;
-    for (int j = 0; j < n_it; ++j) {
-      bool on[2];
-      int lim[2];  // valid columns of the group
+    // Valid columns of step j's two 32-column groups (0: not kept), from the
+    // entries fetched a step before.
+    auto columns = [&](int j, int (&lim)[2]) {
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        ent[g] = next[g];
+        const int ent = next[g];
         const int idx = (j + 1) * EPI + slot[g];
         next[g] = idx < n_ent ? __ldg(p.entry + e0 + idx) : 0;
-        lim[g] = p.L - (ent[g] & 0xFFFF) * BLK - (64 * half + 32 * g) % BLK;
-        on[g] = (((ent[g] >> 16) >> qb) & 1) && lim[g] > 0;
+        const int left = p.L - (ent & 0xFFFF) * BLK - (64 * half + 32 * g) % BLK;
+        lim[g] = ((ent >> 16) >> qb) & 1 ? max(left, 0) : 0;
       }
-      if (!(ok = warp_wait(s_full, j & 1, wc))) break;
+    };
+    // Weights of step j into w, in two groups, the second loaded under the
+    // first one's arithmetic.
+    float w0[32], w1[32];
+    int lim[2];
+    auto weights = [&](int j) -> bool {
+      columns(j, lim);
+      if (!warp_wait(s_full, j & 1, wc)) return false;
       tc_fence_after();
-      float w[64];
-      tmem_ld_64(s_col, w);
+      tmem_ld32(s_col, w0);
+      tmem_ld_wait();
+      tmem_ld32(s_col + 32, w1);
+      if (lim[0] > 0) exp2_shifted(w0, p.scale_log2, shift);
       tmem_ld_wait();
       warp_arrive(s_free, lane);
+      if (lim[1] > 0) exp2_shifted(w1, p.scale_log2, shift);
+      return true;
+    };
+    // dS of one group: y = w (dP - D); keys of the padding score 0, whose
+    // weight can overflow.
+    auto gradient = [&](float (&y)[32], const float (&w)[32], int left) {
+      if (left > 0) {
+        add_mul32(y, -delta, w);
+        if (left < 32) {
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        float (&x)[32] = *reinterpret_cast<float(*)[32]>(&w[32 * g]);
-        if (!on[g]) continue;
-        exp2_shifted(x, p.scale_log2, shift);
+          for (int i = 0; i < 32; ++i)
+            if (i >= left) y[i] = 0.f;
+        }
+      } else {
+        zero32(y);
       }
+    };
+    ok = weights(0);
+    for (int j = 0; ok && j < n_it; ++j) {
       if (!(ok = warp_wait(dp_full, j & 1, wc))) break;
       tc_fence_after();
-      float y[64];
-      tmem_ld_64(dp_col, y);
+      float y0[32], y1[32];
+      tmem_ld32(dp_col, y0);
       tmem_ld_wait();
-      const f32x2 nd = f2_make(-delta, -delta);
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        float (&x)[32] = *reinterpret_cast<float(*)[32]>(&y[32 * g]);
-        if (on[g]) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            f2_split(f2_mul(f2_add(f2_make(x[i], x[i + 1]), nd),
-                            f2_make(w[32 * g + i], w[32 * g + i + 1])), x[i], x[i + 1]);
-          if (lim[g] < 32) {
-            // Keys of the padding score 0, whose weight can overflow.
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i >= lim[g]) x[i] = 0.f;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = 0.f;
-        }
-        tmem_st_bf16(dp_col + 16 * g, x);
-      }
+      tmem_ld32(dp_col + 32, y1);
+      gradient(y0, w0, lim[0]);
+      tmem_st_bf16(dp_col, y0);
+      tmem_ld_wait();
       tmem_st_wait();
-      warp_arrive(ds_full, lane);
+      warp_arrive(&ds_full[0], lane);
+      gradient(y1, w1, lim[1]);
+      tmem_st_bf16(dp_col + 16, y1);
+      tmem_st_wait();
+      warp_arrive(&ds_full[1], lane);
+      if (j + 1 < n_it) ok = weights(j + 1);
     }
     if (ok && (ok = warp_wait(acc_full, 0, wc))) {
       tc_fence_after();
