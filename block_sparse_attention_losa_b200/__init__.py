@@ -145,12 +145,16 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.bfloat16:
+def _dtype_code_of(dtype: torch.dtype) -> int:
+    if dtype == torch.bfloat16:
         return LOSA_BF16
-    if t.dtype == torch.float32:
+    if dtype == torch.float32:
         return LOSA_FP32
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    raise TypeError(f"unsupported dtype {dtype}")
+
+
+def _dtype_code(t: torch.Tensor) -> int:
+    return _dtype_code_of(t.dtype)
 
 
 def _check_qkv(q, k, v):
@@ -348,14 +352,26 @@ def sparse_attn(q, k, v, L, pattern: Pattern, scale=None, out_dtype=torch.float3
 
 
 def _on(stream, device):
-    """The context of a call's own allocations: `device`, and `stream` if one
-    is given, so that a workspace freed on return is reused in that stream's
-    order."""
+    """The context of a call's own allocations and launch: `device`, and
+    `stream` if one is given, so that a workspace freed on return is reused in
+    that stream's order. Nothing to enter in the usual case."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return _HERE_AND_NOW
     stack = contextlib.ExitStack()
     stack.enter_context(torch.cuda.device(device))
     if stream is not None:
         stack.enter_context(torch.cuda.stream(stream))
     return stack
+
+
+_HERE_AND_NOW = contextlib.nullcontext()
+
+
+def _raw_stream(stream, device):
+    """The cudaStream_t of `stream`, by default the device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def sparse_attn_bwd(q, k, v, o, lse, do, L, pattern: Pattern, scale=None, out_dtype=None,
@@ -366,42 +382,44 @@ def sparse_attn_bwd(q, k, v, o, lse, do, L, pattern: Pattern, scale=None, out_dt
     have q's dtype unless out_dtype or the outputs say otherwise. Rows >= L of
     the inputs are not used; those of the results are 0."""
     _check_qkv(q, k, v)
-    B, H, Lp, d = q.shape
+    shape, device = q.shape, q.device
+    B, H, Lp, d = shape
     if (B, H, Lp) != (pattern.B, pattern.H, pattern.n_blocks * pattern.block):
         raise ValueError("q/k/v shape does not match the pattern")
     for name, t in (("o", o), ("do", do)):
-        if not (t.device == q.device and t.is_contiguous() and t.shape == q.shape):
+        if not (t.shape == shape and t.device == device and t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous tensor of q's shape and device")
-    if not (lse.device == q.device and lse.is_contiguous() and lse.dtype == torch.float32
-            and lse.shape == q.shape[:3]):
+    if not (lse.shape == shape[:3] and lse.dtype == torch.float32 and lse.device == device
+            and lse.is_contiguous()):
         raise ValueError("lse must be a contiguous fp32 tensor [B, H, L_pad] on q's device")
-    if not (q.device == k.device == v.device == torch.device(pattern.device)):
+    if not device == k.device == v.device == pattern.device:
         raise ValueError("q, k, v and the pattern must be on one device")
     scale = default_scale(d) if scale is None else scale
     given = [t for t in (dq, dk, dv) if t is not None]
     if out_dtype is None:
         out_dtype = given[0].dtype if given else q.dtype
     for t in given:
-        if not (t.device == q.device and t.is_contiguous() and t.shape == q.shape
-                and t.dtype == out_dtype):
+        if not (t.shape == shape and t.dtype == out_dtype and t.device == device
+                and t.is_contiguous()):
             raise ValueError("dq, dk, dv must be contiguous tensors of q's shape and device "
                              "and of one dtype")
-    with _on(stream, q.device):
-        dq, dk, dv = (torch.empty(q.shape, device=q.device, dtype=out_dtype) if t is None else t
-                      for t in (dq, dk, dv))
-        need = _lib.losa_sparse_attn_bwd_workspace(pattern.handle, _dtype_code(q),
-                                                   _dtype_code(do), d)
-        if need < 0:
-            _check("losa_sparse_attn_bwd_workspace", int(need))
+    in_code, do_code = _dtype_code(q), _dtype_code(do)
+    need = _lib.losa_sparse_attn_bwd_workspace(pattern.handle, in_code, do_code, d)
+    if need < 0:
+        _check("losa_sparse_attn_bwd_workspace", need)
+    with _on(stream, device):
+        if len(given) < 3:
+            dq, dk, dv = (torch.empty(shape, device=device, dtype=out_dtype) if t is None else t
+                          for t in (dq, dk, dv))
         if workspace is None:
-            workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
-        elif not (workspace.device == q.device and workspace.is_contiguous()):
+            workspace = torch.empty(need, device=device, dtype=torch.uint8)
+        elif not (workspace.device == device and workspace.is_contiguous()):
             raise ValueError("workspace must be a contiguous tensor on q's device")
         st = _lib.losa_sparse_attn_bwd(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), o.data_ptr(), _dtype_code(o),
-            lse.data_ptr(), do.data_ptr(), _dtype_code(do), d, int(L), float(scale),
-            pattern.handle, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _dtype_code(dq),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), in_code, o.data_ptr(), _dtype_code(o),
+            lse.data_ptr(), do.data_ptr(), do_code, d, int(L), float(scale), pattern.handle,
+            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _dtype_code(dq), workspace.data_ptr(),
+            workspace.nbytes, _raw_stream(stream, device))
     _check("losa_sparse_attn_bwd", st)
     return dq, dk, dv
 
@@ -439,6 +457,7 @@ class Rope:
                              (ctypes.c_int * 3)(*map(int, pad(start, 0))),
                              (ctypes.c_double * 3)(*map(float, pad(scale, 1.0))), float(theta),
                              int(n_text), ("interleaved", "halves").index(pairing))
+        self.ref = ctypes.byref(self.spec)
 
 
 def _check_positions(positions, B, L, rope, device):
@@ -451,27 +470,40 @@ def _check_positions(positions, B, L, rope, device):
     return positions.data_ptr()
 
 
-def _same(name, tensors, n_dims):
-    """The one device, shape and dtype of a call's tensors (None left out)."""
-    some = [t for t in tensors if t is not None]
-    if not some:
+def _same(name, tensors):
+    """The first of a call's 4-dimensional tensors (None left out), after a
+    check that all have its device, shape and dtype."""
+    first = None
+    for t in tensors:
+        if t is None:
+            continue
+        if first is None:
+            first = t
+            if not (t.is_cuda and t.dim() == 4):
+                raise ValueError(f"{name} must be CUDA tensors of 4 dimensions")
+            shape, dtype, device = t.shape, t.dtype, t.device
+        elif not (t.shape == shape and t.dtype == dtype and t.device == device):
+            raise ValueError(f"{name} must be of one shape, dtype and device")
+    if first is None:
         raise ValueError(f"one of {name} must be given")
-    for t in some:
-        if not (t.is_cuda and t.dim() == n_dims and t.shape == some[0].shape
-                and t.dtype == some[0].dtype and t.device == some[0].device):
-            raise ValueError(f"{name} must be CUDA tensors of one shape, dtype and device")
-    return some[0]
+    return first
+
+
+_Strides = ctypes.c_int64 * 9
 
 
 def _token_strides(tensors):
-    flat = (ctypes.c_int64 * 9)()
-    for i, t in enumerate(tensors):
+    """The (batch, token, head) strides of a call's three tensors."""
+    flat = []
+    for t in tensors:
         if t is None:
+            flat += (0, 0, 0)
             continue
-        if t.shape[3] > 1 and t.stride(3) != 1:
+        b, l, h, f = t.stride()
+        if f != 1 and t.shape[3] > 1:
             raise ValueError("features must be adjacent in memory (stride 1)")
-        flat[3 * i:3 * i + 3] = [t.stride(0), t.stride(1), t.stride(2)]
-    return flat
+        flat += (b, l, h)
+    return _Strides(*flat)
 
 
 _ptr = lambda t: None if t is None else t.data_ptr()
@@ -483,29 +515,32 @@ def rope_pack(q, k, v, block, rope: Rope, positions=None, out_dtype=None, out=No
     [B, H, L_pad, d], L_pad the next multiple of `block`, padded rows 0. Any
     of the three may be None. positions: int32 [B, L, axes] instead of the
     rope's grid and start. out: the three tensors to write."""
-    x = _same("q, k, v", (q, k, v), 4)
+    x = _same("q, k, v", (q, k, v))
     B, L, H, d = x.shape
     if block not in (32, 64, 128):
         raise ValueError("block must be 32, 64 or 128")
-    Lp = (L + block - 1) // block * block
+    Lp = -(-L // block) * block
+    device, dtype = x.device, out_dtype or x.dtype
     strides = _token_strides((q, k, v))
-    pos = _check_positions(positions, B, L, rope, x.device)
-    with _on(stream, x.device):
+    pos = _check_positions(positions, B, L, rope, device)
+    with _on(stream, device):
         if out is None:
             out = tuple(None if t is None else
-                        torch.empty(B, H, Lp, d, device=x.device, dtype=out_dtype or x.dtype)
+                        torch.empty((B, H, Lp, d), device=device, dtype=dtype)
                         for t in (q, k, v))
-        y = _same("out", out, 4)
-        if any((a is None) != (b is None) for a, b in zip((q, k, v), out)):
-            raise ValueError("out must have a tensor for each of q, k, v that is given")
-        if y.device != x.device or y.shape != (B, H, Lp, d) or \
-                any(t is not None and not t.is_contiguous() for t in out) or \
-                (out_dtype is not None and y.dtype != out_dtype):
-            raise ValueError("out must be contiguous [B, H, L_pad, d] tensors on the inputs' "
-                             "device")
+        else:
+            y = _same("out", out)
+            if [t is None for t in (q, k, v)] != [t is None for t in out]:
+                raise ValueError("out must have a tensor for each of q, k, v that is given")
+            if y.device != device or y.shape != (B, H, Lp, d) or \
+                    any(t is not None and not t.is_contiguous() for t in out) or \
+                    (out_dtype is not None and y.dtype != out_dtype):
+                raise ValueError("out must be contiguous [B, H, L_pad, d] tensors on the "
+                                 "inputs' device")
+            dtype = y.dtype
         st = _lib.losa_rope_pack(_ptr(q), _ptr(k), _ptr(v), _dtype_code(x), strides, B, H, L, Lp,
-                                 d, ctypes.byref(rope.spec), pos, *map(_ptr, out), _dtype_code(y),
-                                 _stream(stream))
+                                 d, rope.ref, pos, *map(_ptr, out), _dtype_code_of(dtype),
+                                 _raw_stream(stream, device))
     _check("losa_rope_pack", st)
     return tuple(out)
 
@@ -515,26 +550,29 @@ def rope_unpack(q, k, v, L, rope: Rope, positions=None, out_dtype=None, out=None
     [B, L, H, d], q and k turned by the negative angle. Any of the three may
     be None (an attention output goes back as v alone). out: the tensors to
     write, of any strides with adjacent features."""
-    x = _same("q, k, v", (q, k, v), 4)
+    x = _same("q, k, v", (q, k, v))
     B, H, Lp, d = x.shape
     L = int(L)
     if any(t is not None and not t.is_contiguous() for t in (q, k, v)):
         raise ValueError("q, k, v must be contiguous [B, H, L_pad, d]")
-    pos = _check_positions(positions, B, L, rope, x.device)
-    with _on(stream, x.device):
+    device, dtype = x.device, out_dtype or x.dtype
+    pos = _check_positions(positions, B, L, rope, device)
+    with _on(stream, device):
         if out is None:
             out = tuple(None if t is None else
-                        torch.empty(B, L, H, d, device=x.device, dtype=out_dtype or x.dtype)
+                        torch.empty((B, L, H, d), device=device, dtype=dtype)
                         for t in (q, k, v))
-        y = _same("out", out, 4)
-        if any((a is None) != (b is None) for a, b in zip((q, k, v), out)):
-            raise ValueError("out must have a tensor for each of q, k, v that is given")
-        if y.device != x.device or y.shape != (B, L, H, d) or \
-                (out_dtype is not None and y.dtype != out_dtype):
-            raise ValueError("out must be [B, L, H, d] tensors on the inputs' device")
+        else:
+            y = _same("out", out)
+            if [t is None for t in (q, k, v)] != [t is None for t in out]:
+                raise ValueError("out must have a tensor for each of q, k, v that is given")
+            if y.device != device or y.shape != (B, L, H, d) or \
+                    (out_dtype is not None and y.dtype != out_dtype):
+                raise ValueError("out must be [B, L, H, d] tensors on the inputs' device")
+            dtype = y.dtype
         st = _lib.losa_rope_unpack(_ptr(q), _ptr(k), _ptr(v), _dtype_code(x), B, H, L, Lp, d,
-                                   ctypes.byref(rope.spec), pos, *map(_ptr, out), _dtype_code(y),
-                                   _token_strides(out), _stream(stream))
+                                   rope.ref, pos, *map(_ptr, out), _dtype_code_of(dtype),
+                                   _token_strides(out), _raw_stream(stream, device))
     _check("losa_rope_unpack", st)
     return tuple(out)
 

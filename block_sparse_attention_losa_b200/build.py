@@ -84,14 +84,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 
 def check_attention_registers(ptxas_log: str, want: int = 168) -> None:
-    """The attention kernels (forward and backward) split their launch registers between
-    warpgroups with setmaxnreg; the split adds up only if every instance
+    """The attention kernels, forward and backward, split their launch
+    registers between warpgroups with setmaxnreg; the split adds up only if every instance
     launches with exactly `want` registers per thread (else a warpgroup
     would wait for registers that never come). Refuse the build otherwise."""
     current, seen = None, 0
     for line in ptxas_log.splitlines():
         if "Compiling entry function" in line:
-            current = any(k in line for k in ("attn_kernel", "bwd_key_kernel", "bwd_query_kernel"))
+            current = any(k in line for k in ("attn_kernel", "bwd_tiles_kernel"))
         elif current and "Used" in line and "registers" in line:
             used = int(line.split("Used")[1].split("registers")[0])
             seen += 1

@@ -1,7 +1,7 @@
-// losa_backward_mma.cu - the tensor-core kernels of losa_sparse_attn_bwd
-// (bf16 operands, fp32 accumulation in tensor memory): one for dK and dV,
-// which owns 128 key rows and walks the query blocks that keep them, and one
-// for dQ, which owns 128 query rows and walks the key blocks they keep.
+// losa_backward_mma.cu - the tensor-core kernel of losa_sparse_attn_bwd
+// (bf16 operands, fp32 accumulation in tensor memory): a CTA owns 128 key
+// rows, for dK and dV, and walks the query blocks that keep them, or 128 query
+// rows, for dQ, and walks the key blocks they keep.
 #include <algorithm>
 
 #include "losa_device.cuh"
@@ -19,14 +19,19 @@ static_assert(2 * 128 * kScoreRegs + 128 * kControlRegs == kBwdThreads * kBwdLau
 constexpr int kTile = 128;  // rows a CTA owns, and rows of a step
 constexpr int kAugBytes = kTile * 32;
 
+// A pattern's lists by key tile or by query tile.
+struct BwdLists {
+  const int *ptr, *entry, *order;
+};
+
 struct BwdParams {
   int L, L_pad, n_qt, n_tiles;
   float scale, scale_log2;
-  const int *ptr, *entry, *order;
+  BwdLists keys, queries;
   const float *lse, *delta;
   const uint16_t *q_aug, *do_aug;
   const void *q, *d_o;  // dQ kernel: its own rows
-  void *out0, *out1;    // dV, dK, or dQ
+  void *dq, *dk, *dv;
   int* status;
   long long wait_limit;
 };
@@ -228,10 +233,9 @@ template <int D> struct KeyLayout {
 // Warps 0-7 hold the scores, thread t of a warp one key row and half the
 // query columns; warp 8 loads, warp 9 issues the MMAs.
 template <int D, int BLK, bool kOutBf16>
-__global__ void __launch_bounds__(kBwdThreads, 1)
-    bwd_key_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                   const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-                   const BwdParams p) {
+__device__ __forceinline__ void key_tile(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                         const CUtensorMap& tm_q, const CUtensorMap& tm_do,
+                                         const BwdParams& p, const BwdLists& list, int tile) {
   using Lay = KeyLayout<D>;
   constexpr int NS = Lay::NS;
   constexpr int EPI = kTile / BLK;  // list entries per step
@@ -260,11 +264,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int tile = p.order[blockIdx.x];
   const int bh = tile / p.n_qt;
   const int kt = tile - bh * p.n_qt;
-  const int e0 = p.ptr[tile];
-  const int n_ent = p.ptr[tile + 1] - e0;
+  const int e0 = list.ptr[tile];
+  const int n_ent = list.ptr[tile + 1] - e0;
   const int n_it = (n_ent + EPI - 1) / EPI;
 
   if (threadIdx.x == 0) {
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         int row[EPI];
 #pragma unroll
         for (int e = 0; e < EPI; ++e)
-          row[e] = (p.entry[e0 + min(j * EPI + e, n_ent - 1)] & 0xFFFF) * BLK;
+          row[e] = (list.entry[e0 + min(j * EPI + e, n_ent - 1)] & 0xFFFF) * BLK;
         auto load = [&](const CUtensorMap* map, const uint16_t* aug, uint64_t* full, int off,
                         int off_aug) {
           mbar_arrive_expect_tx(full, Lay::TILE_BYTES + kAugBytes);
@@ -449,14 +452,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int slot[2] = {(64 * half) / BLK, (64 * half + 32) / BLK};
     int ent[2], next[2];
 #pragma unroll
-    for (int g = 0; g < 2; ++g) next[g] = slot[g] < n_ent ? __ldg(p.entry + e0 + slot[g]) : 0;
+    for (int g = 0; g < 2; ++g) next[g] = slot[g] < n_ent ? __ldg(list.entry + e0 + slot[g]) : 0;
     for (int j = 0; j < n_it; ++j) {
       bool on[2];
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         ent[g] = next[g];
         const int idx = (j + 1) * EPI + slot[g];
-        next[g] = idx < n_ent ? __ldg(p.entry + e0 + idx) : 0;
+        next[g] = idx < n_ent ? __ldg(list.entry + e0 + idx) : 0;
         on[g] = ((ent[g] >> 16) >> kb) & 1;
       }
       if (!(ok = warp_wait(s_full, j & 1, wc))) break;
@@ -508,7 +511,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // ---- results: warps 0-3 dV, warps 4-7 dK; rows of the padding are 0
     const int row = kt * kTile + r;
     const size_t out_at = (size_t(bh) * p.L_pad + row) * D;
-    void* out = half ? p.out1 : p.out0;
+    void* out = half ? p.dk : p.dv;
     if (n_it > 0 && ok && (ok = warp_wait(acc_full, 0, wc))) {
       tc_fence_after();
       const float f = half ? p.scale : 1.f;
@@ -558,9 +561,8 @@ template <int D> struct QueryLayout {
 // as soon as the softmax has S(j) in registers, then dQ(j) and dP(j+1); dS
 // takes dP's place as the A operand of dQ += dS K.
 template <int D, int BLK, bool kOutBf16>
-__global__ void __launch_bounds__(kBwdThreads, 1)
-    bwd_query_kernel(const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, const BwdParams p) {
+__device__ __forceinline__ void query_tile(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                           const BwdParams& p, const BwdLists& list, int tile) {
   using Lay = QueryLayout<D>;
   constexpr int NS = Lay::NS;
   constexpr int EPI = kTile / BLK;
@@ -589,11 +591,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int tile = p.order[blockIdx.x];
   const int bh = tile / p.n_qt;
   const int qt = tile - bh * p.n_qt;
-  const int e0 = p.ptr[tile];
-  const int n_ent = p.ptr[tile + 1] - e0;  // at least 1: every query block keeps one
+  const int e0 = list.ptr[tile];
+  const int n_ent = list.ptr[tile + 1] - e0;  // at least 1: every query block keeps one
   const int n_it = (n_ent + EPI - 1) / EPI;
 
   if (threadIdx.x == 0) {
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         int row[EPI];
 #pragma unroll
         for (int e = 0; e < EPI; ++e)
-          row[e] = (p.entry[e0 + min(j * EPI + e, n_ent - 1)] & 0xFFFF) * BLK;
+          row[e] = (list.entry[e0 + min(j * EPI + e, n_ent - 1)] & 0xFFFF) * BLK;
         auto load = [&](const CUtensorMap* map, uint64_t* full, int off) {
           mbar_arrive_expect_tx(full, Lay::TILE_BYTES);
 #pragma unroll
@@ -761,7 +762,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int slot[2] = {(64 * half) / BLK, (64 * half + 32) / BLK};
     int next[2];
 #pragma unroll
-    for (int g = 0; g < 2; ++g) next[g] = slot[g] < n_ent ? __ldg(p.entry + e0 + slot[g]) : 0;
+    for (int g = 0; g < 2; ++g) next[g] = slot[g] < n_ent ? __ldg(list.entry + e0 + slot[g]) : 0;
     // Valid columns of step j's two 32-column groups (0: not kept), from the
     // entries fetched a step before.
     auto columns = [&](int j, int (&lim)[2]) {
@@ -769,7 +770,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int g = 0; g < 2; ++g) {
         const int ent = next[g];
         const int idx = (j + 1) * EPI + slot[g];
-        next[g] = idx < n_ent ? __ldg(p.entry + e0 + idx) : 0;
+        next[g] = idx < n_ent ? __ldg(list.entry + e0 + idx) : 0;
         const int left = p.L - (ent & 0xFFFF) * BLK - (64 * half + 32 * g) % BLK;
         lim[g] = ((ent >> 16) >> qb) & 1 ? max(left, 0) : 0;
       }
@@ -834,9 +835,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tmem_ld32(at + C_DQ + col, x);
         tmem_ld_wait();
         if (valid)
-          store_row32<kOutBf16>(p.out0, flat * D + col, x, p.scale);
+          store_row32<kOutBf16>(p.dq, flat * D + col, x, p.scale);
         else if (row < p.L_pad)
-          store_zero32<kOutBf16>(p.out0, flat * D + col);
+          store_zero32<kOutBf16>(p.dq, flat * D + col);
       }
     }
   }
@@ -850,45 +851,45 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
 }
 
+// Both halves of the gradient in one launch: the key tiles first, whose steps
+// have four products, then the query tiles, whose steps have three. The
+// query tiles fill the SMs that the last key tiles leave idle, and a small
+// call's two halves run side by side.
 template <int D, int BLK, bool kOutBf16>
-cudaError_t run_mma(const BackwardCall& c, const BackwardOperands& w, BwdParams p,
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    bwd_tiles_kernel(const __grid_constant__ CUtensorMap own_k,
+                     const __grid_constant__ CUtensorMap own_v,
+                     const __grid_constant__ CUtensorMap step_q,
+                     const __grid_constant__ CUtensorMap step_do,
+                     const __grid_constant__ CUtensorMap step_k,
+                     const __grid_constant__ CUtensorMap step_v, const BwdParams p) {
+  const int i = blockIdx.x;
+  if (i < p.n_tiles)
+    key_tile<D, BLK, kOutBf16>(own_k, own_v, step_q, step_do, p, p.keys, p.keys.order[i]);
+  else
+    query_tile<D, BLK, kOutBf16>(step_k, step_v, p, p.queries, p.queries.order[i - p.n_tiles]);
+}
+
+template <int D, int BLK, bool kOutBf16>
+cudaError_t run_mma(const BackwardCall& c, const BackwardOperands& w, const BwdParams& p,
                     cudaStream_t stream) {
-  const losa_pattern* pat = c.p;
-  const int BH = pat->B * pat->H;
-  constexpr int box = BLK;
-  CUtensorMap k_own, v_own, q_step, do_step, k_step, v_step;
+  const int BH = c.p->B * c.p->H;
+  CUtensorMap own_k, own_v, step_q, step_do, step_k, step_v;
   // Rows past L read as zero, whatever they hold.
-  if (!make_slab_map(&k_own, c.k, BH, c.L, p.L_pad, D, kTile, 2, false) ||
-      !make_slab_map(&v_own, c.v, BH, c.L, p.L_pad, D, kTile, 2, false) ||
-      !make_slab_map(&q_step, c.q, BH, c.L, p.L_pad, D, box, 2, false) ||
-      !make_slab_map(&do_step, w.d_o, BH, c.L, p.L_pad, D, box, 2, false) ||
-      !make_slab_map(&k_step, c.k, BH, c.L, p.L_pad, D, box, 2, false) ||
-      !make_slab_map(&v_step, c.v, BH, c.L, p.L_pad, D, box, 2, false))
+  if (!make_slab_map(&own_k, c.k, BH, c.L, p.L_pad, D, kTile, 2, false) ||
+      !make_slab_map(&own_v, c.v, BH, c.L, p.L_pad, D, kTile, 2, false) ||
+      !make_slab_map(&step_q, c.q, BH, c.L, p.L_pad, D, BLK, 2, false) ||
+      !make_slab_map(&step_do, w.d_o, BH, c.L, p.L_pad, D, BLK, 2, false) ||
+      !make_slab_map(&step_k, c.k, BH, c.L, p.L_pad, D, BLK, 2, false) ||
+      !make_slab_map(&step_v, c.v, BH, c.L, p.L_pad, D, BLK, 2, false))
     return cudaErrorInvalidValue;
-  auto keys = bwd_key_kernel<D, BLK, kOutBf16>;
-  auto queries = bwd_query_kernel<D, BLK, kOutBf16>;
-  cudaError_t err = cudaFuncSetAttribute(keys, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         KeyLayout<D>::SMEM_ALLOC);
+  auto kern = bwd_tiles_kernel<D, BLK, kOutBf16>;
+  constexpr int smem = std::max(KeyLayout<D>::SMEM_ALLOC, QueryLayout<D>::SMEM_ALLOC);
+  const cudaError_t err =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
-  err = cudaFuncSetAttribute(queries, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             QueryLayout<D>::SMEM_ALLOC);
-  if (err != cudaSuccess) return err;
-  p.ptr = pat->key_ptr;
-  p.entry = pat->key_entry;
-  p.order = pat->key_order;
-  p.out0 = c.dv;
-  p.out1 = c.dk;
-  keys<<<unsigned(pat->n_tiles), kBwdThreads, KeyLayout<D>::SMEM_ALLOC, stream>>>(
-      k_own, v_own, q_step, do_step, p);
-  err = cudaGetLastError();
-  if (err != cudaSuccess) return err;
-  p.ptr = pat->tile_ptr;
-  p.entry = pat->tile_entry;
-  p.order = pat->tile_order;
-  p.out0 = c.dq;
-  p.out1 = nullptr;
-  queries<<<unsigned(pat->n_tiles), kBwdThreads, QueryLayout<D>::SMEM_ALLOC, stream>>>(
-      k_step, v_step, p);
+  kern<<<2u * unsigned(p.n_tiles), kBwdThreads, smem, stream>>>(own_k, own_v, step_q, step_do,
+                                                               step_k, step_v, p);
   return cudaGetLastError();
 }
 
@@ -910,6 +911,11 @@ cudaError_t launch_backward_mma(const BackwardCall& c, const BackwardOperands& w
   p.do_aug = w.do_aug;
   p.q = c.q;
   p.d_o = w.d_o;
+  p.dq = c.dq;
+  p.dk = c.dk;
+  p.dv = c.dv;
+  p.keys = {pat->key_ptr, pat->key_entry, pat->key_order};
+  p.queries = {pat->tile_ptr, pat->tile_entry, pat->tile_order};
   p.status = device_status_word();
   if (!p.status) return cudaErrorInvalidDevice;
   p.wait_limit = wait_limit();
