@@ -22,9 +22,10 @@ namespace {
 // ------------------------------------------------------------------ D
 
 // D_i = dO_i . O_i, one warp per row; rows of the padding get 0. The sum is
-// held in fp32. With `rounded`, dO (fp32) is first rounded to bf16, the form
-// in which the products of the bf16 path read it, and that copy is written:
-// D then cancels against the same dO that dP is made of.
+// held in fp32. Where dO's type is not that of q, k and v, `copy` receives it
+// in theirs: a fp32 dO is rounded to bf16, as the tensor cores read it, before
+// D is formed, so that D cancels against the same dO that dP is made of; a
+// bf16 one is widened.
 template <int D>
 __device__ __forceinline__ void load_row(const void* base, bool bf16, size_t row, int lane,
                                          float (&v)[D / 32]) {
@@ -69,7 +70,7 @@ struct AugRows {
 template <int D>
 __global__ void __launch_bounds__(256)
     delta_kernel(const void* o, bool o_bf16, const void* d_o, bool do_bf16, int64_t rows,
-                 int L, int L_pad, float* delta, uint16_t* rounded, const AugRows aug) {
+                 int L, int L_pad, float* delta, void* copy, const AugRows aug) {
   const int lane = threadIdx.x & 31;
   const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (row >= rows) return;
@@ -78,13 +79,19 @@ __global__ void __launch_bounds__(256)
     float a[D / 32], b[D / 32];
     load_row<D>(o, o_bf16, row, lane, a);
     load_row<D>(d_o, do_bf16, row, lane, b);
-    if (rounded) {
-      uint32_t* w = reinterpret_cast<uint32_t*>(rounded + row * D + lane * (D / 32));
+    if (copy && do_bf16) {
+      float* w = static_cast<float*>(copy) + row * D + lane * (D / 32);
+#pragma unroll
+      for (int e = 0; e < D / 32; e += 2) *reinterpret_cast<float2*>(w + e) = make_float2(b[e], b[e + 1]);
+    } else if (copy) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(copy) + row * D +
+                                                lane * (D / 32));
 #pragma unroll
       for (int e = 0; e < D / 32; e += 2) {
-        w[e / 2] = pack_bf16x2(b[e], b[e + 1]);
-        b[e] = __uint_as_float(w[e / 2] << 16);
-        b[e + 1] = __uint_as_float(w[e / 2] & 0xffff0000u);
+        const uint32_t u = pack_bf16x2(b[e], b[e + 1]);
+        w[e / 2] = u;
+        b[e] = __uint_as_float(u << 16);
+        b[e + 1] = __uint_as_float(u & 0xffff0000u);
       }
     }
 #pragma unroll
@@ -110,234 +117,284 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------------ fp32
 
-struct SimtParams {
-  const float *q, *k, *v;
-  const void* d_o;
-  bool do_bf16, out_bf16;
-  const float *lse, *delta;
-  int L, L_pad, n_qt, block;
+struct FmaParams {
+  const float *q, *k, *v, *d_o, *lse, *delta;
+  int L, L_pad, n_qt, n_tiles, block;
   float scale;
-  const int *ptr, *entry, *order;
+  const int *key_ptr, *key_entry, *key_order;        // by key tile
+  const int *tile_ptr, *tile_entry, *tile_order;     // by query tile
   void *dq, *dk, *dv;
+  bool out_bf16;
 };
 
-__device__ __forceinline__ float load_value(const void* p, bool bf16, size_t i) {
-  return bf16 ? __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(p) + i)) << 16)
-              : __ldg(static_cast<const float*>(p) + i);
-}
-
-__device__ __forceinline__ void store4(void* p, bool bf16, size_t i, float4 x) {
+__device__ __forceinline__ void store4(void* p, bool bf16, size_t i, const float* x, float f) {
   if (bf16) {
     uint2 w;
-    w.x = pack_bf16x2(x.x, x.y);
-    w.y = pack_bf16x2(x.z, x.w);
+    w.x = pack_bf16x2(x[0] * f, x[1] * f);
+    w.y = pack_bf16x2(x[2] * f, x[3] * f);
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = w;
   } else {
-    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = x;
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) =
+        make_float4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
   }
 }
 
-__device__ __forceinline__ float dot4(const float4& a, const float4& b, float c) {
-  return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, c))));
+// 16 bytes from global to shared memory, asynchronously; zeros if !valid.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
 }
 
-constexpr int kSimtThreads = 256;
-constexpr int kSimtRows = 64;  // rows a CTA owns, and rows per step
+constexpr int kFmaThreads = 256;
+constexpr int kOwn = 32;   // rows a CTA owns
+constexpr int kStep = 64;  // rows of the other side per step
 
-template <int D> struct SimtSmem {
-  float x[kSimtRows][D + 4], x2[kSimtRows][D + 4];  // own rows: K, V or Q, dO
-  float y[kSimtRows][D + 4], y2[kSimtRows][D + 4];  // a step's rows: Q, dO or K, V
-  float p[kSimtRows][kSimtRows + 4], ds[kSimtRows][kSimtRows + 4];  // [step row][own row]
+// All rows hold their 16-byte chunks permuted: chunk c of row r at place
+// c ^ (r & 7), so that eight rows' equal chunks and a row's adjacent chunks
+// both lie in different banks. 112 KB at D = 128: two CTAs per SM.
+template <int D> struct FmaSmem {
+  float x[kOwn][D], x2[kOwn][D];    // own rows: K, V or Q, dO
+  float y[kStep][D], y2[kStep][D];  // a step's rows: Q, dO or K, V
+  float p[kStep][kOwn], ds[kStep][kOwn];
 };
+template <int N>
+__device__ __forceinline__ const float4& chunk(const float (&row)[N], int r, int c) {
+  return *reinterpret_cast<const float4*>(&row[(c ^ (r & 7)) * 4]);
+}
 
-// One CTA owns half of a 128-row tile: 64 key rows (kKeys: dK and dV) or 64
-// query rows (dQ), and walks the tile's list 64 rows of the other side at a
-// time: two segments of 32 rows, the unit in which a block of any size (32,
-// 64, 128) starts and ends. Every product is fp32 FMA: 256 threads hold a
-// 64 x 64 score tile (4 x 4 each) and a 64 x D gradient tile (4 x D / 16
-// each).
+// acc += a . b of four features as two pairs of partial sums.
+__device__ __forceinline__ void dot4(const float4& a, const float4& b, f32x2& acc) {
+  acc = f2_fma(f2_make(a.x, a.y), f2_make(b.x, b.y), acc);
+  acc = f2_fma(f2_make(a.z, a.w), f2_make(b.z, b.w), acc);
+}
+
+// One CTA owns 32 rows (a quarter of a 128-row tile, always inside one block)
+// of keys (kKeys: dK and dV) or of queries (dQ) and walks those list entries
+// whose blocks meet, 64 rows of the other side at a time: two segments of 32
+// rows, the unit in which blocks of 32, 64 and 128 rows start and end.
+// Every product is fp32 FMA, bound by the FMA units and, close behind, by
+// shared-memory reads; the tiles below keep the reads of a warp's operands
+// under its FMA time:
+//   scores: a warp has 16 x 16 of the 32 x 64, a thread 4 x 2 of it;
+//   gradients: a thread has 8 own rows x 4 features; 256 threads hold both
+//   products (keys) and, with what is left, parts of the step's rows, summed
+//   at the end.
 template <int D, bool kKeys>
-__global__ void __launch_bounds__(kSimtThreads)
-    bwd_simt_kernel(const SimtParams p) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  SimtSmem<D>& sm = *reinterpret_cast<SimtSmem<D>*>(smem_raw);
-  constexpr int NC = D / 64;  // float4 groups of a gradient row per thread
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int tile = p.order[blockIdx.x >> 1], half = blockIdx.x & 1;
+__device__ __forceinline__ void fma_tile(const FmaParams& p, FmaSmem<D>& sm, int tile,
+                                         int quarter) {
+  constexpr int CH = D / 4;                                  // chunks of a row
+  constexpr int GROUPS = kFmaThreads / (CH * (kOwn / 8));    // 2 at D = 128, 4 at 64
+  constexpr int PARTS = kKeys ? GROUPS / 2 : GROUPS;         // of a step's rows
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int bh = tile / p.n_qt;
-  const int own0 = (tile - bh * p.n_qt) * 128 + half * 64;
+  const int own0 = (tile - bh * p.n_qt) * 128 + quarter * kOwn;
   if (own0 >= p.L_pad) return;
   const size_t base = size_t(bh) * p.L_pad;
-  const int e1 = p.ptr[tile + 1];
+  const int* ptr = kKeys ? p.key_ptr : p.tile_ptr;
+  const int* entry = kKeys ? p.key_entry : p.tile_entry;
+  const unsigned bit = 1u << (16 + quarter * kOwn / p.block);
   const int per_entry = p.block / 32;
+  int e = ptr[tile], part = 0;
+  const int e1 = own0 < p.L ? ptr[tile + 1] : e;  // padding alone: nothing to sum
 
-  auto fill = [&](float (&dst)[kSimtRows][D + 4], const void* src, bool bf16, int r0, int first,
-                  int rows) {
-    for (int i = tid; i < rows * D; i += kSimtThreads) {
-      const int r = i / D, c = i - r * D;
-      dst[first + r][c] =
-          (r0 >= 0 && r0 + r < p.L) ? load_value(src, bf16, (base + r0 + r) * D + c) : 0.f;
+  // First row of the list's next segment of 32 rows, -1 at its end.
+  auto next_segment = [&]() -> int {
+    while (e < e1) {
+      const int ent = __ldg(entry + e);
+      if (unsigned(ent) & bit) {
+        const int row = (ent & 0xFFFF) * p.block + part * 32;
+        if (++part == per_entry) part = 0, ++e;
+        if (row < p.L) return row;
+      } else {
+        ++e;
+      }
+    }
+    return -1;
+  };
+  auto fill = [&](float* dst, const float* src, int r0, int rows) {
+    for (int i = tid; i < rows * CH; i += kFmaThreads) {
+      const int r = i / CH, c = i - r * CH;
+      const bool in = r0 >= 0 && r0 + r < p.L;
+      copy16(dst + r * D + (c ^ (r & 7)) * 4, src + (base + (in ? r0 + r : 0)) * D + c * 4, in);
     }
   };
-  fill(sm.x, kKeys ? p.k : p.q, false, own0, 0, kSimtRows);
-  fill(sm.x2, kKeys ? p.v : p.d_o, kKeys ? false : p.do_bf16, own0, 0, kSimtRows);
+  fill(&sm.x[0][0], kKeys ? p.k : p.q, own0, kOwn);
+  fill(&sm.x2[0][0], kKeys ? p.v : p.d_o, own0, kOwn);
 
-  float acc[4][NC * 4] = {}, acc2[kKeys ? 4 : 1][NC * 4] = {};
+  // Scores: own rows 16 (warp / 4) + lane / 8 + 4 a, step rows 16 (warp % 4)
+  // + lane % 8 + 8 i.
+  const int so = 16 * (warp >> 2) + (lane >> 3), si = 16 * (warp & 3) + (lane & 7);
+  // Gradients: own rows 8 go.. and chunk gc, for the group's product and part.
+  const int group = tid / (CH * (kOwn / 8)), within = tid % (CH * (kOwn / 8));
+  const int go = 8 * (within / CH), gc = within % CH;
+  const bool use_p = kKeys && (group & 1);
+  const int gpart = kKeys ? group >> 1 : group;
+  f32x2 acc[8][2] = {};
   float own_lse[4], own_delta[4];
   if (!kKeys) {
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
-      const int r = own0 + ty * 4 + a;
+      const int r = own0 + so + 4 * a;
       own_lse[a] = r < p.L ? p.lse[base + r] : 0.f;
       own_delta[a] = r < p.L ? p.delta[base + r] : 0.f;
     }
   }
 
-  // The list's segments that touch this half, two at a time.
-  int e = p.ptr[tile], part = 0;
-  while (true) {
-    int row0[2] = {-1, -1};
-    bool keep[2][2] = {};  // [segment][32-row group of the own rows]
+  int seg[2] = {next_segment(), next_segment()};
+  while (seg[0] >= 0) {
+    const int row0[2] = {seg[0], seg[1]};
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      while (e < e1 && row0[s] < 0) {
-        const int ent = p.entry[e];
-        const unsigned m = unsigned(ent) >> 16;
-        const bool k0 = (m >> ((half * 2) * 32 / p.block)) & 1;
-        const bool k1 = (m >> ((half * 2 + 1) * 32 / p.block)) & 1;
-        if (k0 || k1) {
-          row0[s] = (ent & 0xFFFF) * p.block + part * 32;
-          keep[s][0] = k0;
-          keep[s][1] = k1;
-          if (++part == per_entry) part = 0, ++e;
-        } else {
-          ++e;
-        }
-      }
+      fill(&sm.y[32 * s][0], kKeys ? p.q : p.k, row0[s], 32);
+      fill(&sm.y2[32 * s][0], kKeys ? p.d_o : p.v, row0[s], 32);
     }
-    if (row0[0] < 0) break;
-    __syncthreads();  // the step before has read y, y2, p and ds
+    float step_lse[2], step_delta[2];
+    bool on[2];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      fill(sm.y, kKeys ? p.q : p.k, false, row0[s], 32 * s, 32);
-      fill(sm.y2, kKeys ? p.d_o : p.v, kKeys ? p.do_bf16 : false, row0[s], 32 * s, 32);
+    for (int i = 0; i < 2; ++i) {
+      const int r = si + 8 * i, row = row0[r >> 5] + (r & 31);
+      on[i] = row0[r >> 5] >= 0 && row < p.L;
+      step_lse[i] = kKeys && on[i] ? __ldg(p.lse + base + row) : 0.f;
+      step_delta[i] = kKeys && on[i] ? __ldg(p.delta + base + row) : 0.f;
     }
+    seg[0] = next_segment();
+    seg[1] = next_segment();
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-    // Scores and dP: own rows 4 ty + a, step rows tx + 16 c.
-    float s_[4][4] = {}, dp[4][4] = {};
-    for (int c = 0; c < D; c += 4) {
-      float4 xv[4], yv[4];
+    f32x2 s2[4][2] = {}, d2[4][2] = {};
+#pragma unroll 2
+    for (int c = 0; c < CH; ++c) {
+      float4 xv[4], yv[2];
 #pragma unroll
-      for (int a = 0; a < 4; ++a) xv[a] = *reinterpret_cast<const float4*>(&sm.x[ty * 4 + a][c]);
+      for (int a = 0; a < 4; ++a) xv[a] = chunk(sm.x[so + 4 * a], so + 4 * a, c);
 #pragma unroll
-      for (int a = 0; a < 4; ++a) yv[a] = *reinterpret_cast<const float4*>(&sm.y[tx + 16 * a][c]);
-#pragma unroll
-      for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          s_[a][i] = dot4(xv[a], yv[i], s_[a][i]);
-#pragma unroll
-      for (int a = 0; a < 4; ++a) xv[a] = *reinterpret_cast<const float4*>(&sm.x2[ty * 4 + a][c]);
-#pragma unroll
-      for (int a = 0; a < 4; ++a) yv[a] = *reinterpret_cast<const float4*>(&sm.y2[tx + 16 * a][c]);
+      for (int i = 0; i < 2; ++i) yv[i] = chunk(sm.y[si + 8 * i], si + 8 * i, c);
 #pragma unroll
       for (int a = 0; a < 4; ++a)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          dp[a][i] = dot4(xv[a], yv[i], dp[a][i]);
+        for (int i = 0; i < 2; ++i) dot4(xv[a], yv[i], s2[a][i]);
+#pragma unroll
+      for (int a = 0; a < 4; ++a) xv[a] = chunk(sm.x2[so + 4 * a], so + 4 * a, c);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) yv[i] = chunk(sm.y2[si + 8 * i], si + 8 * i, c);
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) dot4(xv[a], yv[i], d2[a][i]);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = tx + 16 * i, s = r >> 5;
-      const int row = row0[s] + (r & 31);
-      const bool in = row0[s] >= 0 && row < p.L;
-      const float lse_i = kKeys && in ? p.lse[base + row] : 0.f;
-      const float delta_i = kKeys && in ? p.delta[base + row] : 0.f;
+    for (int i = 0; i < 2; ++i) {
+      const int r = si + 8 * i;
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
-        const int own = ty * 4 + a;
-        const bool on = in && keep[s][own >> 5] && own0 + own < p.L;
+        const int o = so + 4 * a;
         // expf, not ex2.approx of a product: dQ is a sum in which the keys'
         // mean cancels, which magnifies a rounding of the exponent.
-        const float x = fmaf(s_[a][i], p.scale, -(kKeys ? lse_i : own_lse[a]));
-        const float w = on ? expf(x) : 0.f;
-        sm.p[r][own] = w;
-        sm.ds[r][own] = on ? w * (dp[a][i] - (kKeys ? delta_i : own_delta[a])) : 0.f;
+        const float x = fmaf(f2_sum(s2[a][i]), p.scale, -(kKeys ? step_lse[i] : own_lse[a]));
+        const float w = on[i] && own0 + o < p.L ? expf(x) : 0.f;
+        const float g = f2_sum(d2[a][i]) - (kKeys ? step_delta[i] : own_delta[a]);
+        const int at = o ^ (4 * (r & 7));
+        if (kKeys) sm.p[r][at] = w;
+        sm.ds[r][at] = w != 0.f ? w * g : 0.f;
       }
     }
     __syncthreads();
-    // acc += dS^T y (dK or dQ), acc2 += P^T y2 (dV): own rows 4 ty + a,
-    // features 4 tx + 64 c.
-    for (int r = 0; r < kSimtRows; ++r) {
-      const float4 ds4 = *reinterpret_cast<const float4*>(&sm.ds[r][ty * 4]);
-      const float dsa[4] = {ds4.x, ds4.y, ds4.z, ds4.w};
+#pragma unroll 4
+    for (int r = gpart * (kStep / PARTS); r < (gpart + 1) * (kStep / PARTS); ++r) {
+      const float(&row)[kOwn] = use_p ? sm.p[r] : sm.ds[r];
+      const float4 a0 = chunk(row, r, go / 4), a1 = chunk(row, r, go / 4 + 1);
+      const float4 yv = use_p ? chunk(sm.y2[r], r, gc) : chunk(sm.y[r], r, gc);
+      const f32x2 y01 = f2_make(yv.x, yv.y), y23 = f2_make(yv.z, yv.w);
+      const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const float4 yv = *reinterpret_cast<const float4*>(&sm.y[r][tx * 4 + 64 * c]);
-        const float ya[4] = {yv.x, yv.y, yv.z, yv.w};
-#pragma unroll
-        for (int a = 0; a < 4; ++a)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[a][c * 4 + i] = fmaf(dsa[a], ya[i], acc[a][c * 4 + i]);
-      }
-      if constexpr (kKeys) {
-        const float4 p4 = *reinterpret_cast<const float4*>(&sm.p[r][ty * 4]);
-        const float pa[4] = {p4.x, p4.y, p4.z, p4.w};
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const float4 yv = *reinterpret_cast<const float4*>(&sm.y2[r][tx * 4 + 64 * c]);
-          const float ya[4] = {yv.x, yv.y, yv.z, yv.w};
-#pragma unroll
-          for (int a = 0; a < 4; ++a)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc2[a][c * 4 + i] = fmaf(pa[a], ya[i], acc2[a][c * 4 + i]);
-        }
+      for (int a = 0; a < 8; ++a) {
+        const f32x2 aa = f2_make(av[a], av[a]);
+        acc[a][0] = f2_fma(aa, y01, acc[a][0]);
+        acc[a][1] = f2_fma(aa, y23, acc[a][1]);
       }
     }
+    __syncthreads();  // before the next step's rows arrive
   }
 
+  // Parts of a gradient meet in shared memory; the first one writes the rows.
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  float out[8][4];
 #pragma unroll
-  for (int a = 0; a < 4; ++a) {
-    const int row = own0 + ty * 4 + a;
-    if (row >= p.L_pad) continue;
-    const float f = row < p.L ? p.scale : 0.f;
+  for (int a = 0; a < 8; ++a) {
+    f2_split(acc[a][0], out[a][0], out[a][1]);
+    f2_split(acc[a][1], out[a][2], out[a][3]);
+  }
+  if constexpr (PARTS > 1) {
+    constexpr int PER = CH * (kOwn / 8) * (kKeys ? 2 : 1);  // threads of a part
+    const int mine = kKeys ? within + (group & 1) * (PER / 2) : within;
+    float4* buf = reinterpret_cast<float4*>(&sm.y[0][0]);
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const size_t at = (base + row) * D + tx * 4 + 64 * c;
-      store4(kKeys ? p.dk : p.dq, p.out_bf16, at,
-             make_float4(acc[a][c * 4] * f, acc[a][c * 4 + 1] * f, acc[a][c * 4 + 2] * f,
-                         acc[a][c * 4 + 3] * f));
-      if constexpr (kKeys)
-        store4(p.dv, p.out_bf16, at, make_float4(acc2[a][c * 4], acc2[a][c * 4 + 1],
-                                                 acc2[a][c * 4 + 2], acc2[a][c * 4 + 3]));
+    for (int s = 1; s < PARTS; ++s) {
+      if (gpart == s) {
+#pragma unroll
+        for (int a = 0; a < 8; ++a)
+          buf[a * PER + mine] = make_float4(out[a][0], out[a][1], out[a][2], out[a][3]);
+      }
+      __syncthreads();
+      if (gpart == 0) {
+#pragma unroll
+        for (int a = 0; a < 8; ++a) {
+          const float4 z = buf[a * PER + mine];
+          out[a][0] += z.x, out[a][1] += z.y, out[a][2] += z.z, out[a][3] += z.w;
+        }
+      }
+      __syncthreads();
+    }
+  }
+  if (gpart == 0) {
+    void* dst = kKeys ? (use_p ? p.dv : p.dk) : p.dq;
+#pragma unroll
+    for (int a = 0; a < 8; ++a) {
+      const int row = own0 + go + a;
+      if (row < p.L_pad)
+        store4(dst, p.out_bf16, (base + row) * D + gc * 4, out[a],
+               row >= p.L ? 0.f : use_p ? 1.f : p.scale);
     }
   }
 }
 
-template <int D, bool kKeys>
-cudaError_t run_simt(const SimtParams& p, int64_t tiles, cudaStream_t stream) {
-  auto kern = bwd_simt_kernel<D, kKeys>;
-  const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               int(sizeof(SimtSmem<D>)));
+// The key quarters of all tiles, longest lists first within a head, then the
+// query quarters.
+template <int D>
+__global__ void __launch_bounds__(kFmaThreads, 2) bwd_fma_kernel(const FmaParams p) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  FmaSmem<D>& sm = *reinterpret_cast<FmaSmem<D>*>(smem_raw);
+  const int i = blockIdx.x >> 2, quarter = blockIdx.x & 3;
+  if (i < p.n_tiles)
+    fma_tile<D, true>(p, sm, p.key_order[i], quarter);
+  else
+    fma_tile<D, false>(p, sm, p.tile_order[i - p.n_tiles], quarter);
+}
+
+template <int D> cudaError_t run_fma(const FmaParams& p, cudaStream_t stream) {
+  const cudaError_t err = cudaFuncSetAttribute(
+      bwd_fma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(FmaSmem<D>)));
   if (err != cudaSuccess) return err;
-  kern<<<unsigned(2 * tiles), kSimtThreads, sizeof(SimtSmem<D>), stream>>>(p);
+  bwd_fma_kernel<D><<<8u * unsigned(p.n_tiles), kFmaThreads, sizeof(FmaSmem<D>), stream>>>(p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 namespace {
-// Offsets of a call's workspace: D, the bf16 path's further operand rows and
-// its bf16 copy of a fp32 dO. Rows come in multiples of 32, so each part is
-// aligned to 128 bytes.
+// Offsets of a call's workspace: D, the bf16 path's further operand rows, and
+// dO in the type of q, k and v where it has the other one. Rows come in
+// multiples of 32, so each part is aligned to 128 bytes.
 struct Workspace {
-  size_t q_aug, do_aug, rounded, bytes;
+  size_t q_aug, do_aug, copy, bytes;
   Workspace(const losa_pattern* p, int d, bool in_bf16, bool do_bf16) {
     const size_t rows = size_t(p->B) * p->H * p->n_blocks * p->block;
     q_aug = rows * 4;
     do_aug = q_aug + (in_bf16 ? rows * 32 : 0);
-    rounded = do_aug + (in_bf16 ? rows * 32 : 0);
-    bytes = rounded + (in_bf16 && !do_bf16 ? rows * d * 2 : 0);
+    copy = do_aug + (in_bf16 ? rows * 32 : 0);
+    bytes = copy + (in_bf16 != do_bf16 ? rows * d * (in_bf16 ? 2 : 4) : 0);
   }
 };
 }  // namespace
@@ -353,50 +410,46 @@ cudaError_t launch_backward(const BackwardCall& c, cudaStream_t stream) {
   const Workspace at(pat, c.d, c.in_bf16, c.do_bf16);
   char* ws = static_cast<char*>(c.workspace);
   float* delta = reinterpret_cast<float*>(ws);
-  uint16_t* rounded =
-      c.in_bf16 && !c.do_bf16 ? reinterpret_cast<uint16_t*>(ws + at.rounded) : nullptr;
+  void* copy = c.in_bf16 != c.do_bf16 ? ws + at.copy : nullptr;
+  const void* d_o = copy ? copy : c.d_o;
   AugRows aug{};
   if (c.in_bf16)
     aug = {reinterpret_cast<uint4*>(ws + at.q_aug), reinterpret_cast<uint4*>(ws + at.do_aug), c.lse,
            1.f / c.scale};
   const unsigned grid = unsigned((rows + 7) / 8);
   (c.d == 64 ? delta_kernel<64> : delta_kernel<128>)<<<grid, 256, 0, stream>>>(
-      c.o, c.o_bf16, c.d_o, c.do_bf16, rows, c.L, L_pad, delta, rounded, aug);
+      c.o, c.o_bf16, c.d_o, c.do_bf16, rows, c.L, L_pad, delta, copy, aug);
   cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   if (c.in_bf16)
-    return launch_backward_mma(c, {rounded ? rounded : c.d_o, delta,
+    return launch_backward_mma(c, {d_o, delta,
                                    reinterpret_cast<const uint16_t*>(ws + at.q_aug),
                                    reinterpret_cast<const uint16_t*>(ws + at.do_aug)},
                                stream);
-  SimtParams p{};
+  FmaParams p{};
   p.q = static_cast<const float*>(c.q);
   p.k = static_cast<const float*>(c.k);
   p.v = static_cast<const float*>(c.v);
-  p.d_o = c.d_o;
-  p.do_bf16 = c.do_bf16;
-  p.out_bf16 = c.out_bf16;
+  p.d_o = static_cast<const float*>(d_o);
   p.lse = c.lse;
   p.delta = delta;
   p.L = c.L;
   p.L_pad = L_pad;
   p.n_qt = pat->n_qt;
+  p.n_tiles = int(pat->n_tiles);
   p.block = pat->block;
   p.scale = c.scale;
+  p.key_ptr = pat->key_ptr;
+  p.key_entry = pat->key_entry;
+  p.key_order = pat->key_order;
+  p.tile_ptr = pat->tile_ptr;
+  p.tile_entry = pat->tile_entry;
+  p.tile_order = pat->tile_order;
   p.dq = c.dq;
   p.dk = c.dk;
   p.dv = c.dv;
-  p.ptr = pat->key_ptr;
-  p.entry = pat->key_entry;
-  p.order = pat->key_order;
-  err = c.d == 64 ? run_simt<64, true>(p, pat->n_tiles, stream)
-                  : run_simt<128, true>(p, pat->n_tiles, stream);
-  if (err != cudaSuccess) return err;
-  p.ptr = pat->tile_ptr;
-  p.entry = pat->tile_entry;
-  p.order = pat->tile_order;
-  return c.d == 64 ? run_simt<64, false>(p, pat->n_tiles, stream)
-                   : run_simt<128, false>(p, pat->n_tiles, stream);
+  p.out_bf16 = c.out_bf16;
+  return c.d == 64 ? run_fma<64>(p, stream) : run_fma<128>(p, stream);
 }
 
 }  // namespace losa
