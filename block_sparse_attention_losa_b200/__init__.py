@@ -409,7 +409,7 @@ def sparse_attn_bwd(q, k, v, o, lse, do, L, pattern: Pattern, scale=None, out_dt
         _check("losa_sparse_attn_bwd_workspace", need)
     with _on(stream, device):
         if len(given) < 3:
-            dq, dk, dv = (torch.empty(shape, device=device, dtype=out_dtype) if t is None else t
+            dq, dk, dv = (torch.empty_like(q, dtype=out_dtype) if t is None else t
                           for t in (dq, dk, dv))
         if workspace is None:
             workspace = torch.empty(need, device=device, dtype=torch.uint8)

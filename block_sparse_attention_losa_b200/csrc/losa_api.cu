@@ -2,6 +2,7 @@
 // word, the fp32 entry conversion, and pattern ownership.
 #include <cmath>
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cstring>
 #include <mutex>
@@ -61,12 +62,17 @@ void* pool_alloc(size_t bytes, cudaStream_t stream) {
 }
 
 bool is_sm100() {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices];  // 0 not asked yet, 1 no, 2 yes
   int dev = 0, major = 0, minor = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  if (const int k = known[dev].load(std::memory_order_relaxed)) return k == 2;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
     return false;
-  return major == 10 && minor == 0;
+  const bool yes = major == 10 && minor == 0;
+  known[dev].store(yes ? 2 : 1, std::memory_order_relaxed);
+  return yes;
 }
 
 namespace {

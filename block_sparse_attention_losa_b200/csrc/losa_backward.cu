@@ -146,23 +146,17 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool valid) {
                : "memory");
 }
 
-constexpr int kFmaThreads = 256;
 constexpr int kOwn = 32;   // rows a CTA owns
 constexpr int kStep = 64;  // rows of the other side per step
 
-// All rows hold their 16-byte chunks permuted: chunk c of row r at place
-// c ^ (r & 7), so that eight rows' equal chunks and a row's adjacent chunks
-// both lie in different banks. 112 KB at D = 128: two CTAs per SM.
+// Own rows are padded by one 16-byte chunk, and the others hold their chunks
+// permuted (chunk c of row r at place c ^ (r & 7)), so that eight rows' equal
+// chunks lie in different banks. 113 KB at D = 128: just two CTAs per SM.
 template <int D> struct FmaSmem {
-  float x[kOwn][D], x2[kOwn][D];    // own rows: K, V or Q, dO
+  float x[kOwn][D + 4], x2[kOwn][D + 4];  // own rows: K, V or Q, dO
   float y[kStep][D], y2[kStep][D];  // a step's rows: Q, dO or K, V
   float p[kStep][kOwn], ds[kStep][kOwn];
 };
-template <int N>
-__device__ __forceinline__ const float4& chunk(const float (&row)[N], int r, int c) {
-  return *reinterpret_cast<const float4*>(&row[(c ^ (r & 7)) * 4]);
-}
-
 // acc += a . b of four features as two pairs of partial sums.
 __device__ __forceinline__ void dot4(const float4& a, const float4& b, f32x2& acc) {
   acc = f2_fma(f2_make(a.x, a.y), f2_make(b.x, b.y), acc);
@@ -173,19 +167,25 @@ __device__ __forceinline__ void dot4(const float4& a, const float4& b, f32x2& ac
 // of keys (kKeys: dK and dV) or of queries (dQ) and walks those list entries
 // whose blocks meet, 64 rows of the other side at a time: two segments of 32
 // rows, the unit in which blocks of 32, 64 and 128 rows start and end.
-// Every product is fp32 FMA, bound by the FMA units and, close behind, by
-// shared-memory reads; the tiles below keep the reads of a warp's operands
-// under its FMA time:
-//   scores: a warp has 16 x 16 of the 32 x 64, a thread 4 x 2 of it;
-//   gradients: a thread has 8 own rows x 4 features; 256 threads hold both
+// Every product is fp32 FMA, and what bounds it is the reads of its operands
+// from shared memory (a 16-byte read of a warp takes two cycles of the SM's
+// shared memory even where its lanes ask for little), so few threads hold
+// large tiles. With T = 128:
+//   scores: a warp has 16 x 32 of the 32 x 64, a thread 4 x 4 of it;
+//   gradients: a thread has 8 own rows x 8 features; the threads hold both
 //   products (keys) and, with what is left, parts of the step's rows, summed
 //   at the end.
-template <int D, bool kKeys>
+// 5,000 tokens, 8 heads, d 64, half the blocks kept: 2.47 ms, 26 TFLOP/s of
+// the five products that the gradient needs, 37 of the seven that run.
+template <int D, int T, bool kKeys>
 __device__ __forceinline__ void fma_tile(const FmaParams& p, FmaSmem<D>& sm, int tile,
                                          int quarter) {
-  constexpr int CH = D / 4;                                  // chunks of a row
-  constexpr int GROUPS = kFmaThreads / (CH * (kOwn / 8));    // 2 at D = 128, 4 at 64
-  constexpr int PARTS = kKeys ? GROUPS / 2 : GROUPS;         // of a step's rows
+  constexpr int CH = D / 4;                           // chunks of a row
+  constexpr int PER = CH / 2 * (kOwn / 8);            // threads that hold a gradient
+  constexpr int GROUPS = T / PER;
+  constexpr int PARTS = kKeys ? GROUPS / 2 : GROUPS;  // of a step's rows
+  constexpr int WARP_ROWS = kStep / (T / 64);         // step rows of a warp's scores
+  constexpr int NI = WARP_ROWS / 8;                   // of a thread's
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int bh = tile / p.n_qt;
   const int own0 = (tile - bh * p.n_qt) * 128 + quarter * kOwn;
@@ -195,42 +195,57 @@ __device__ __forceinline__ void fma_tile(const FmaParams& p, FmaSmem<D>& sm, int
   const int* entry = kKeys ? p.key_entry : p.tile_entry;
   const unsigned bit = 1u << (16 + quarter * kOwn / p.block);
   const int per_entry = p.block / 32;
-  int e = ptr[tile], part = 0;
+  int e = ptr[tile];
   const int e1 = own0 < p.L ? ptr[tile + 1] : e;  // padding alone: nothing to sum
 
+  // The list's entries, 32 at a time in the lanes of each warp (one by one,
+  // each would cost a load's latency), and the next 32.
+  auto entries = [&](int at) { return at + lane < e1 ? __ldg(entry + at + lane) : 0; };
+  int word = 0, ahead = entries(e), ent = 0, part = 0;
+  unsigned meets = 0;  // lanes of `word` whose block meets the own rows
   // First row of the list's next segment of 32 rows, -1 at its end.
   auto next_segment = [&]() -> int {
-    while (e < e1) {
-      const int ent = __ldg(entry + e);
-      if (unsigned(ent) & bit) {
-        const int row = (ent & 0xFFFF) * p.block + part * 32;
-        if (++part == per_entry) part = 0, ++e;
-        if (row < p.L) return row;
-      } else {
-        ++e;
+    while (true) {
+      if (part == 0) {
+        while (meets == 0) {
+          if (e >= e1) return -1;
+          word = ahead;
+          meets = __ballot_sync(0xffffffffu, (unsigned(word) & bit) != 0);
+          e += 32;
+          ahead = entries(e);
+        }
+        ent = __shfl_sync(0xffffffffu, word, __ffs(meets) - 1);
+        meets &= meets - 1;
       }
+      const int row = (ent & 0xFFFF) * p.block + part * 32;
+      if (++part == per_entry) part = 0;
+      if (row < p.L) return row;
     }
-    return -1;
   };
-  auto fill = [&](float* dst, const float* src, int r0, int rows) {
-    for (int i = tid; i < rows * CH; i += kFmaThreads) {
-      const int r = i / CH, c = i - r * CH;
+  // 32 rows from r0 on (none if r0 < 0), rows of the padding as zeros.
+  auto fill = [&](float* dst, const float* src, int r0, bool padded) {
+#pragma unroll
+    for (int n = 0; n < 32 * CH / T; ++n) {
+      const int r = (tid + n * T) / CH, c = tid % CH;
       const bool in = r0 >= 0 && r0 + r < p.L;
-      copy16(dst + r * D + (c ^ (r & 7)) * 4, src + (base + (in ? r0 + r : 0)) * D + c * 4, in);
+      copy16(dst + (padded ? r * (D + 4) + c * 4 : r * D + (c ^ (r & 7)) * 4),
+             src + (base + (in ? r0 + r : 0)) * D + c * 4, in);
     }
   };
-  fill(&sm.x[0][0], kKeys ? p.k : p.q, own0, kOwn);
-  fill(&sm.x2[0][0], kKeys ? p.v : p.d_o, own0, kOwn);
+  fill(&sm.x[0][0], kKeys ? p.k : p.q, own0, true);
+  fill(&sm.x2[0][0], kKeys ? p.v : p.d_o, own0, true);
 
-  // Scores: own rows 16 (warp / 4) + lane / 8 + 4 a, step rows 16 (warp % 4)
-  // + lane % 8 + 8 i.
-  const int so = 16 * (warp >> 2) + (lane >> 3), si = 16 * (warp & 3) + (lane & 7);
-  // Gradients: own rows 8 go.. and chunk gc, for the group's product and part.
-  const int group = tid / (CH * (kOwn / 8)), within = tid % (CH * (kOwn / 8));
-  const int go = 8 * (within / CH), gc = within % CH;
+  // Scores: the warp's 16 own rows and WARP_ROWS step rows, the thread's rows
+  // so + 4 a and si + 8 i.
+  const int so = 16 * (warp / (T / 64)) + (lane >> 3);
+  const int si = WARP_ROWS * (warp % (T / 64)) + (lane & 7);
+  // Gradients: own rows go.. and chunks gc and gc + CH / 2, for the group's
+  // product and part.
+  const int group = tid / PER, within = tid % PER;
+  const int go = 8 * (within / (CH / 2)), gc = within % (CH / 2);
   const bool use_p = kKeys && (group & 1);
   const int gpart = kKeys ? group >> 1 : group;
-  f32x2 acc[8][2] = {};
+  f32x2 acc[4][8] = {};  // pairs of own rows x features
   float own_lse[4], own_delta[4];
   if (!kKeys) {
 #pragma unroll
@@ -246,15 +261,17 @@ __device__ __forceinline__ void fma_tile(const FmaParams& p, FmaSmem<D>& sm, int
     const int row0[2] = {seg[0], seg[1]};
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      fill(&sm.y[32 * s][0], kKeys ? p.q : p.k, row0[s], 32);
-      fill(&sm.y2[32 * s][0], kKeys ? p.d_o : p.v, row0[s], 32);
+      fill(&sm.y[32 * s][0], kKeys ? p.q : p.k, row0[s], false);
+      fill(&sm.y2[32 * s][0], kKeys ? p.d_o : p.v, row0[s], false);
     }
-    float step_lse[2], step_delta[2];
-    bool on[2];
+    // A warp's step rows lie in one segment.
+    float step_lse[NI], step_delta[NI];
+    bool on[NI];
+    const int seg0 = si >= 32 ? row0[1] : row0[0];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = si + 8 * i, row = row0[r >> 5] + (r & 31);
-      on[i] = row0[r >> 5] >= 0 && row < p.L;
+    for (int i = 0; i < NI; ++i) {
+      const int row = seg0 + (si & 31) + 8 * i;
+      on[i] = seg0 >= 0 && row < p.L;
       step_lse[i] = kKeys && on[i] ? __ldg(p.lse + base + row) : 0.f;
       step_delta[i] = kKeys && on[i] ? __ldg(p.delta + base + row) : 0.f;
     }
@@ -262,29 +279,30 @@ __device__ __forceinline__ void fma_tile(const FmaParams& p, FmaSmem<D>& sm, int
     seg[1] = next_segment();
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-    f32x2 s2[4][2] = {}, d2[4][2] = {};
+    f32x2 s2[4][NI] = {}, d2[4][NI] = {};
 #pragma unroll 2
     for (int c = 0; c < CH; ++c) {
-      float4 xv[4], yv[2];
+      const int yc = (c ^ (si & 7)) * 4;
+      float4 xv[4], yv[NI];
 #pragma unroll
-      for (int a = 0; a < 4; ++a) xv[a] = chunk(sm.x[so + 4 * a], so + 4 * a, c);
+      for (int a = 0; a < 4; ++a) xv[a] = *reinterpret_cast<const float4*>(&sm.x[so + 4 * a][4 * c]);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) yv[i] = chunk(sm.y[si + 8 * i], si + 8 * i, c);
-#pragma unroll
-      for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) dot4(xv[a], yv[i], s2[a][i]);
-#pragma unroll
-      for (int a = 0; a < 4; ++a) xv[a] = chunk(sm.x2[so + 4 * a], so + 4 * a, c);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) yv[i] = chunk(sm.y2[si + 8 * i], si + 8 * i, c);
+      for (int i = 0; i < NI; ++i) yv[i] = *reinterpret_cast<const float4*>(&sm.y[si + 8 * i][yc]);
 #pragma unroll
       for (int a = 0; a < 4; ++a)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) dot4(xv[a], yv[i], d2[a][i]);
+        for (int i = 0; i < NI; ++i) dot4(xv[a], yv[i], s2[a][i]);
+#pragma unroll
+      for (int a = 0; a < 4; ++a) xv[a] = *reinterpret_cast<const float4*>(&sm.x2[so + 4 * a][4 * c]);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) yv[i] = *reinterpret_cast<const float4*>(&sm.y2[si + 8 * i][yc]);
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int i = 0; i < NI; ++i) dot4(xv[a], yv[i], d2[a][i]);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NI; ++i) {
       const int r = si + 8 * i;
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
@@ -300,18 +318,25 @@ __device__ __forceinline__ void fma_tile(const FmaParams& p, FmaSmem<D>& sm, int
       }
     }
     __syncthreads();
+    const float* wts = use_p ? &sm.p[0][0] : &sm.ds[0][0];
+    const float* rows = use_p ? &sm.y2[0][0] : &sm.y[0][0];
 #pragma unroll 4
     for (int r = gpart * (kStep / PARTS); r < (gpart + 1) * (kStep / PARTS); ++r) {
-      const float(&row)[kOwn] = use_p ? sm.p[r] : sm.ds[r];
-      const float4 a0 = chunk(row, r, go / 4), a1 = chunk(row, r, go / 4 + 1);
-      const float4 yv = use_p ? chunk(sm.y2[r], r, gc) : chunk(sm.y[r], r, gc);
-      const f32x2 y01 = f2_make(yv.x, yv.y), y23 = f2_make(yv.z, yv.w);
-      const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+      const int k = r & 7;
+      const float4 a0 = *reinterpret_cast<const float4*>(wts + r * kOwn + (go ^ (4 * k)));
+      const float4 a1 = *reinterpret_cast<const float4*>(wts + r * kOwn + ((go + 4) ^ (4 * k)));
+      const f32x2 av[4] = {f2_make(a0.x, a0.y), f2_make(a0.z, a0.w), f2_make(a1.x, a1.y),
+                           f2_make(a1.z, a1.w)};
 #pragma unroll
-      for (int a = 0; a < 8; ++a) {
-        const f32x2 aa = f2_make(av[a], av[a]);
-        acc[a][0] = f2_fma(aa, y01, acc[a][0]);
-        acc[a][1] = f2_fma(aa, y23, acc[a][1]);
+      for (int n = 0; n < 2; ++n) {
+        const float4 yv =
+            *reinterpret_cast<const float4*>(rows + r * D + ((gc ^ k) + n * (CH / 2)) * 4);
+        const f32x2 yy[4] = {f2_make(yv.x, yv.x), f2_make(yv.y, yv.y), f2_make(yv.z, yv.z),
+                             f2_make(yv.w, yv.w)};
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[a][4 * n + i] = f2_fma(av[a], yy[i], acc[a][4 * n + i]);
       }
     }
     __syncthreads();  // before the next step's rows arrive
@@ -320,30 +345,36 @@ __device__ __forceinline__ void fma_tile(const FmaParams& p, FmaSmem<D>& sm, int
   // Parts of a gradient meet in shared memory; the first one writes the rows.
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  float out[8][4];
+  float out[8][8];
 #pragma unroll
-  for (int a = 0; a < 8; ++a) {
-    f2_split(acc[a][0], out[a][0], out[a][1]);
-    f2_split(acc[a][1], out[a][2], out[a][3]);
-  }
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f2_split(acc[a][i], out[2 * a][i], out[2 * a + 1][i]);
   if constexpr (PARTS > 1) {
-    constexpr int PER = CH * (kOwn / 8) * (kKeys ? 2 : 1);  // threads of a part
-    const int mine = kKeys ? within + (group & 1) * (PER / 2) : within;
+    constexpr int N = PER * (kKeys ? 2 : 1);  // threads of a part
+    const int mine = within + (use_p ? PER : 0);
     float4* buf = reinterpret_cast<float4*>(&sm.y[0][0]);
+    static_assert(16 * N * sizeof(float4) <= sizeof(sm.y), "room for a part's sums");
 #pragma unroll
     for (int s = 1; s < PARTS; ++s) {
       if (gpart == s) {
 #pragma unroll
         for (int a = 0; a < 8; ++a)
-          buf[a * PER + mine] = make_float4(out[a][0], out[a][1], out[a][2], out[a][3]);
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            buf[(2 * a + n) * N + mine] =
+                make_float4(out[a][4 * n], out[a][4 * n + 1], out[a][4 * n + 2], out[a][4 * n + 3]);
       }
       __syncthreads();
       if (gpart == 0) {
 #pragma unroll
-        for (int a = 0; a < 8; ++a) {
-          const float4 z = buf[a * PER + mine];
-          out[a][0] += z.x, out[a][1] += z.y, out[a][2] += z.z, out[a][3] += z.w;
-        }
+        for (int a = 0; a < 8; ++a)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const float4 z = buf[(2 * a + n) * N + mine];
+            out[a][4 * n] += z.x, out[a][4 * n + 1] += z.y;
+            out[a][4 * n + 2] += z.z, out[a][4 * n + 3] += z.w;
+          }
       }
       __syncthreads();
     }
@@ -353,31 +384,33 @@ __device__ __forceinline__ void fma_tile(const FmaParams& p, FmaSmem<D>& sm, int
 #pragma unroll
     for (int a = 0; a < 8; ++a) {
       const int row = own0 + go + a;
-      if (row < p.L_pad)
-        store4(dst, p.out_bf16, (base + row) * D + gc * 4, out[a],
-               row >= p.L ? 0.f : use_p ? 1.f : p.scale);
+      if (row >= p.L_pad) continue;
+      const float f = row >= p.L ? 0.f : use_p ? 1.f : p.scale;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+        store4(dst, p.out_bf16, (base + row) * D + (gc + n * (CH / 2)) * 4, &out[a][4 * n], f);
     }
   }
 }
 
 // The key quarters of all tiles, longest lists first within a head, then the
 // query quarters.
-template <int D>
-__global__ void __launch_bounds__(kFmaThreads, 2) bwd_fma_kernel(const FmaParams p) {
+template <int D, int T>
+__global__ void __launch_bounds__(T, T == 128 ? 2 : 1) bwd_fma_kernel(const FmaParams p) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   FmaSmem<D>& sm = *reinterpret_cast<FmaSmem<D>*>(smem_raw);
   const int i = blockIdx.x >> 2, quarter = blockIdx.x & 3;
   if (i < p.n_tiles)
-    fma_tile<D, true>(p, sm, p.key_order[i], quarter);
+    fma_tile<D, T, true>(p, sm, p.key_order[i], quarter);
   else
-    fma_tile<D, false>(p, sm, p.tile_order[i - p.n_tiles], quarter);
+    fma_tile<D, T, false>(p, sm, p.tile_order[i - p.n_tiles], quarter);
 }
 
-template <int D> cudaError_t run_fma(const FmaParams& p, cudaStream_t stream) {
+template <int D, int T> cudaError_t run_fma(const FmaParams& p, cudaStream_t stream) {
   const cudaError_t err = cudaFuncSetAttribute(
-      bwd_fma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(FmaSmem<D>)));
+      bwd_fma_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(FmaSmem<D>)));
   if (err != cudaSuccess) return err;
-  bwd_fma_kernel<D><<<8u * unsigned(p.n_tiles), kFmaThreads, sizeof(FmaSmem<D>), stream>>>(p);
+  bwd_fma_kernel<D, T><<<8u * unsigned(p.n_tiles), T, sizeof(FmaSmem<D>), stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -449,7 +482,13 @@ cudaError_t launch_backward(const BackwardCall& c, cudaStream_t stream) {
   p.dk = c.dk;
   p.dv = c.dv;
   p.out_bf16 = c.out_bf16;
-  return c.d == 64 ? run_fma<64>(p, stream) : run_fma<128>(p, stream);
+  // Few CTAs (up to two per SM): a CTA's own speed counts, and 256 threads
+  // hide more latency (600 tokens, 4 heads, d 128, 160 CTAs: 76 us against 103
+  // with 128). Many: the larger tiles of 128 threads read less shared memory
+  // (1,200 tokens, 320 CTAs: 183 us against 199).
+  if (8 * pat->n_tiles <= 2 * 148)
+    return c.d == 64 ? run_fma<64, 256>(p, stream) : run_fma<128, 256>(p, stream);
+  return c.d == 64 ? run_fma<64, 128>(p, stream) : run_fma<128, 128>(p, stream);
 }
 
 }  // namespace losa
