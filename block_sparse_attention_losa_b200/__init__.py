@@ -17,6 +17,9 @@ Training and the layout around it:
     pat.prepare_backward()                                     # once per pattern
     dq, dk, dv = losa.sparse_attn_bwd(q, k, v, o, lse, do, L, pat)
     dxq, dxk, dxv = losa.rope_unpack(dq, dk, dv, L, rope)      # packed -> [B, L, heads, d]
+
+    out, state = losa.layer_attn(xq, xk, xv, rope, pat)        # the same in one call each way
+    dxq, dxk, dxv = losa.layer_attn_bwd(dout, state)
 """
 from __future__ import annotations
 
@@ -24,6 +27,7 @@ import contextlib
 import ctypes
 import math
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -575,6 +579,49 @@ def rope_unpack(q, k, v, L, rope: Rope, positions=None, out_dtype=None, out=None
                                    _token_strides(out), _raw_stream(stream, device))
     _check("losa_rope_unpack", st)
     return tuple(out)
+
+
+class LayerState(NamedTuple):
+    """What layer_attn keeps for layer_attn_bwd: packed Q, K, V and O, the row
+    log-sum-exp and the call's settings."""
+    q: torch.Tensor
+    k: torch.Tensor
+    v: torch.Tensor
+    o: torch.Tensor
+    lse: torch.Tensor
+    L: int
+    rope: Rope
+    pattern: Pattern
+    positions: torch.Tensor
+    scale: float
+
+
+def layer_attn(q, k, v, rope: Rope, pattern: Pattern, positions=None, scale=None, stream=None):
+    """A later step's attention from a layer's projections to its output
+    projection's input: q, k, v [B, L, H, d] (rope_pack's) are turned and
+    packed, attend over the frozen pattern, and O returns to [B, L, H, d] in
+    q's dtype. Returns (out, state); state is layer_attn_bwd's."""
+    L = q.shape[1]
+    with _on(stream, q.device):
+        qp, kp, vp = rope_pack(q, k, v, pattern.block, rope, positions=positions, stream=stream)
+        # O stays fp32 for the backward pass, whose D = dO . O cancels against
+        # dP; the layer's output is rounded once.
+        o, lse = sparse_attn(qp, kp, vp, L, pattern, scale=scale, stream=stream)
+        out = rope_unpack(None, None, o, L, rope, out_dtype=q.dtype, stream=stream)[2]
+    return out, LayerState(qp, kp, vp, o, lse, L, rope, pattern, positions, scale)
+
+
+def layer_attn_bwd(dout, state: LayerState, out=None, stream=None):
+    """Gradients of layer_attn's q, k, v [B, L, H, d] from dout, the gradient
+    of its output (any strides, features adjacent). out: the three tensors to
+    write, for instance views of one fused gradient."""
+    s = state
+    with _on(stream, dout.device):
+        do = rope_pack(None, None, dout, s.pattern.block, s.rope, positions=s.positions,
+                       stream=stream)[2]
+        grads = sparse_attn_bwd(s.q, s.k, s.v, s.o, s.lse, do, s.L, s.pattern, scale=s.scale,
+                                stream=stream)
+        return rope_unpack(*grads, s.L, s.rope, positions=s.positions, out=out, stream=stream)
 
 
 def exp2_eval(x, stream=None):

@@ -234,51 +234,69 @@ def test_against_differences_of_the_forward_call(losa, dtype):
         assert (got - want).abs().item() <= 12e-3 * R.double().norm().item() + 0.05 * size
 
 
-def test_training_step_through_rope_and_graph(losa):
-    """pack, forward, backward and unpack as a training step runs them: the
-    gradients with respect to the token-major projections against a plain
-    formulation's, and the captured step's bits against the eager one's."""
-    B, H, d, grid, block, L = 1, 3, 128, (3, 10, 13), 64, 390
-    rope = losa.Rope(grid, (44, 42, 42))
+def plain_layer(x, mask, block, grid, dims):
+    """The layer in 64 bits, differentiable: x [B, L, 3, H, d] projections."""
+    B, L, _, H, d = x.shape
+    pos = torch.stack(torch.meshgrid(*(torch.arange(m, device="cuda") for m in grid),
+                                     indexing="ij"), -1).reshape(-1, 3).double()
+    ang = torch.cat([pos[:, a, None] * 10000.0 ** (-torch.arange(0, m, 2, device="cuda") / m)
+                     for a, m in enumerate(dims)], 1)[None, :, None]
+    qkv = torch.view_as_complex(x.unflatten(-1, (d // 2, 2)))
+    turn = torch.polar(torch.ones_like(ang), ang)
+    q, k = (torch.view_as_real(qkv[:, :, i] * turn).flatten(-2).transpose(1, 2) for i in (0, 1))
+    v = x[:, :, 2].transpose(1, 2)
+    keep = token_mask(mask, block, L).cuda().view(B, H, L, L)
+    s = torch.where(keep, q @ k.transpose(2, 3) / math.sqrt(d), -math.inf)
+    return (torch.softmax(s, -1) @ v).transpose(1, 2)
+
+
+@pytest.mark.parametrize("whole", [True, False])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_training_step(losa, whole, dtype):
+    """pack, forward, backward and unpack as a training step runs them, call
+    by call and through layer_attn and layer_attn_bwd: the gradients with
+    respect to the token-major projections against a plain formulation's, and
+    (bf16, whose forward call allocates nothing of its own) two captured
+    steps' bits against the eager one's."""
+    B, H, d, grid, dims, block, L = 2, 3, 128, (3, 10, 13), (44, 42, 42), 64, 390
+    rope = losa.Rope(grid, dims)
     g = torch.Generator("cuda").manual_seed(4)
     n = -(-L // block)
-    mask = make_mask(H, n, 0.5, torch.Generator().manual_seed(6))
+    mask = make_mask(B * H, n, 0.5, torch.Generator().manual_seed(6))
     pat = pattern_of(losa, mask, B, H, block)
-    x = torch.randn(B, L, 3, H, d, generator=g, device="cuda").to(BF)
-    dout = torch.randn(B, L, H, d, generator=g, device="cuda").to(BF)
+    x = torch.randn(B, L, 3, H, d, generator=g, device="cuda").to(dtype)
+    dout = torch.randn(B, L, H, d, generator=g, device="cuda").to(dtype)
 
     def step(x, dout):
+        dx = torch.empty_like(x)
+        if whole:
+            out, state = losa.layer_attn(*x.unbind(2), rope, pat)
+            losa.layer_attn_bwd(dout, state, out=dx.unbind(2))
+            return out, dx
         q, k, v = losa.rope_pack(*x.unbind(2), block, rope)
         o, lse = losa.sparse_attn(q, k, v, L, pat)
-        out = losa.rope_unpack(None, None, o, L, rope, out_dtype=BF)[2]
+        out = losa.rope_unpack(None, None, o, L, rope, out_dtype=dtype)[2]
         do = losa.rope_pack(None, None, dout, block, rope)[2]
         grads = losa.sparse_attn_bwd(q, k, v, o, lse, do, L, pat)
-        dx = torch.empty_like(x)
         losa.rope_unpack(*grads, L, rope, out=dx.unbind(2))
         return out, dx
 
     out, dx = step(x, dout)
     losa.check_status()
-    # Plain, in 64 bits and on the unrounded path from x.
     y = x.double().requires_grad_()
-    pos = torch.stack(torch.meshgrid(*(torch.arange(m, device="cuda") for m in grid),
-                                     indexing="ij"), -1).reshape(-1, 3).double()
-    ang = torch.cat([pos[:, a, None] * 10000.0 ** (-torch.arange(0, m, 2, device="cuda") / m)
-                     for a, m in enumerate((44, 42, 42))], 1)[None, :, None]
-    qkv = torch.view_as_complex(y.unflatten(-1, (d // 2, 2)))
-    turn = torch.polar(torch.ones_like(ang), ang)
-    q, k = (torch.view_as_real(qkv[:, :, i] * turn).flatten(-2).transpose(1, 2) for i in (0, 1))
-    v = y[:, :, 2].transpose(1, 2)
-    keep = token_mask(mask, block, L).cuda()[None]
-    s = torch.where(keep, q @ k.transpose(2, 3) / math.sqrt(d), -math.inf)
-    ref = (torch.softmax(s, -1) @ v).transpose(1, 2)
+    ref = plain_layer(y, mask, block, grid, dims)
     ref.backward(dout.double())
-    # Roundings to bf16 on the way of a gradient: q and k, P, dS, dq/dk, dx,
-    # each at most 2^-8 of its value; they add as norms, and q and k's also
-    # through the scores (|s| up to 5 here, e^(5 * 2^-8)): below 8 half steps.
+    # bf16: roundings on the way of a gradient: q and k, P, dS, dq/dk, dx, each
+    # at most 2^-8 of its value; they add as norms, and q and k's also through
+    # the scores (|s| up to 5 here, e^(5 * 2^-8)): below 8 half steps. fp32:
+    # the forward call's operands and weights are tf32 (half a step 2^-11),
+    # which reaches the gradient through O and lse: the same count of those.
+    unit = V if dtype == BF else 2.0 ** -11
     rel = lambda a, b: ((a.double() - b).norm() / b.norm()).item()
-    assert rel(out, ref) <= 8 * V
-    assert rel(dx, y.grad) <= 8 * V
+    assert rel(out, ref) <= 8 * unit
+    assert rel(dx, y.grad) <= 8 * unit
+    if dtype != BF:
+        return
     static, sd = torch.zeros_like(x), torch.zeros_like(dout)
     graphs = []
     for _ in range(2):  # two captured steps, each with its own memory
@@ -292,6 +310,47 @@ def test_training_step_through_rope_and_graph(losa):
         graph.replay()
     for _, (o2, dx2) in graphs:
         assert torch.equal(o2, out) and torch.equal(dx2, dx)
+
+
+def test_layer_on_another_stream_and_positions(losa):
+    """The whole layer on a side stream, with positions listed per clip that
+    repeat the grid's, gives the default stream's bits."""
+    B, H, d, grid, block, L = 2, 2, 64, (2, 5, 9), 32, 90
+    mask = make_mask(B * H, 3, 0.7, torch.Generator().manual_seed(2))
+    pat = pattern_of(losa, mask, B, H, block)
+    rope = losa.Rope(grid, (16, 24, 24))
+    x = torch.randn(B, L, 3, H, d, device="cuda").to(BF)
+    dout = torch.randn(B, L, H, d, device="cuda").to(BF)
+    out, state = losa.layer_attn(*x.unbind(2), rope, pat)
+    want = losa.layer_attn_bwd(dout, state)
+    pos = torch.stack(torch.meshgrid(*(torch.arange(m) for m in grid), indexing="ij"),
+                      -1).reshape(1, -1, 3).int().repeat(B, 1, 1).cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out2, state2 = losa.layer_attn(*x.unbind(2), rope, pat, positions=pos, stream=side)
+    got = losa.layer_attn_bwd(dout, state2, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(out, out2)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_a_wait_that_runs_out(losa):
+    """With a wait limit of one cycle the call gives up, the status says so,
+    and the next call is whole again."""
+    B, H, d, L, block = 1, 2, 128, 1000, 64
+    mask = make_mask(2, 16, 0.5, torch.Generator().manual_seed(8))
+    pat = pattern_of(losa, mask, B, H, block)
+    args, ref, tol = inputs(B, H, L, 1024, d, BF, F32, BF, mask, block, 31)
+    try:
+        losa.set_wait_limit(1)
+        losa.sparse_attn_bwd(*args, L, pat)
+        with pytest.raises(losa.LosaError) as e:
+            losa.check_status()
+        assert e.value.status == -4
+    finally:
+        losa.set_wait_limit(0)
+    close(losa.sparse_attn_bwd(*args, L, pat), ref, tol, L)
+    losa.check_status()
 
 
 def test_two_streams_at_once(losa):
