@@ -482,11 +482,12 @@ cudaError_t launch_backward(const BackwardCall& c, cudaStream_t stream) {
   p.dk = c.dk;
   p.dv = c.dv;
   p.out_bf16 = c.out_bf16;
-  // Few CTAs (up to two per SM): a CTA's own speed counts, and 256 threads
-  // hide more latency (600 tokens, 4 heads, d 128, 160 CTAs: 76 us against 103
-  // with 128). Many: the larger tiles of 128 threads read less shared memory
-  // (1,200 tokens, 320 CTAs: 183 us against 199).
-  if (8 * pat->n_tiles <= 2 * 148)
+  // At most one CTA per SM or a few more: a CTA's own speed counts, and 256
+  // threads hide more latency (600 tokens, 4 heads, d 128, 160 CTAs: 76 us
+  // against 103 with 128). More: two CTAs of 128 threads share an SM, and their
+  // larger tiles read less shared memory (3,048 tokens, one head, d 64, 192
+  // CTAs: 343 us against 404).
+  if (8 * pat->n_tiles <= 148 + 148 / 8)
     return c.d == 64 ? run_fma<64, 256>(p, stream) : run_fma<128, 256>(p, stream);
   return c.d == 64 ? run_fma<64, 128>(p, stream) : run_fma<128, 128>(p, stream);
 }

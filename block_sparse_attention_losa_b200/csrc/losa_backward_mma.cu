@@ -225,10 +225,11 @@ template <int D> struct KeyLayout {
 // K and V matching columns of ones, so S^T arrives as q.k - lse / scale and
 // dP^T as dO.v - D for 1/8 of a product's time each.
 //
-// Per step j the MMA thread issues dV(j), S(j+1), dK(j), dP(j+1): the
-// softmax's first half (P from S) runs under dK(j-1) and dP(j), its second
-// (dS from P and dP) under dV(j) and S(j+1), with one buffer of each in the
-// 512 columns of tensor memory: S/P, dP/dS, dV, dK.
+// Per step j the MMA warp issues dV(j), S(j+1), dK(j), dP(j+1): the softmax's
+// first half (P from S) runs under dK(j-1) and dP(j), its second (dS from P
+// and dP) under dV(j) and S(j+1), with one buffer of each in the 512 columns
+// of tensor memory: S/P, dP/dS, dV, dK. At D = 64 there is room for a second
+// S/P, and S(j+1) comes first.
 //
 // Warps 0-7 hold the scores, thread t of a warp one key row and half the
 // query columns; warp 8 loads, warp 9 issues the MMAs.
@@ -240,7 +241,11 @@ __device__ __forceinline__ void key_tile(const CUtensorMap& tm_k, const CUtensor
   constexpr int NS = Lay::NS;
   constexpr int EPI = kTile / BLK;  // list entries per step
   constexpr int SLABS = D / 64;
-  constexpr uint32_t C_S = 0, C_DP = 128, C_DV = 256, C_DK = 256 + D;
+  constexpr uint32_t C_DP = 128, C_DV = 256, C_DK = 256 + D;
+  // S and P of step j: at D = 64 two buffers fit, and S(j+1) is formed while
+  // step j's are in use.
+  constexpr bool kTwoS = D == 64;
+  auto c_s = [](int j) -> uint32_t { return kTwoS && (j & 1) ? 384u : 0u; };
   constexpr uint32_t IDESC_S = idesc_bf16_f32(kTile, kTile, false, false);
   constexpr uint32_t IDESC_G = idesc_bf16_f32(kTile, D, false, true);
 
@@ -403,7 +408,7 @@ __device__ __forceinline__ void key_tile(const CUtensorMap& tm_k, const CUtensor
       bool ok = warp_wait(kv_full, 0, wc) && warp_wait(&q_full[0], 0, wc);
       if (ok) {
         tc_fence_after();
-        issue_scores(C_S, Lay::OFF_K, Lay::OFF_Q, Lay::OFF_QA, 0, s_full);
+        issue_scores(c_s(0), Lay::OFF_K, Lay::OFF_Q, Lay::OFF_QA, 0, s_full);
         ok = warp_wait(&do_full[0], 0, wc);
       }
       if (ok) {
@@ -413,17 +418,20 @@ __device__ __forceinline__ void key_tile(const CUtensorMap& tm_k, const CUtensor
       for (int j = 0; ok && j < n_it; ++j) {
         const int st = j % NS, nx = (j + 1) % NS;
         const uint32_t nx_parity = ((j + 1) / NS) & 1;
+        auto next_scores = [&]() -> bool {
+          if (!warp_wait(&q_full[nx], nx_parity, wc)) return false;
+          tc_fence_after();
+          issue_scores(c_s(j + 1), Lay::OFF_K, Lay::OFF_Q, Lay::OFF_QA, nx, s_full);
+          return true;
+        };
+        if (kTwoS && j + 1 < n_it && !(ok = next_scores())) break;
         if (!(ok = warp_wait(&p_full[0], j & 1, wc))) break;
         tc_fence_after();
-        issue_grad(C_DV, C_S, Lay::OFF_DO, st, 0, j == 0, nullptr);
+        issue_grad(C_DV, c_s(j), Lay::OFF_DO, st, 0, j == 0, nullptr);
         if (!(ok = warp_wait(&p_full[1], j & 1, wc))) break;
         tc_fence_after();
-        issue_grad(C_DV, C_S, Lay::OFF_DO, st, 1, false, &do_empty[st]);
-        if (j + 1 < n_it) {
-          if (!(ok = warp_wait(&q_full[nx], nx_parity, wc))) break;
-          tc_fence_after();
-          issue_scores(C_S, Lay::OFF_K, Lay::OFF_Q, Lay::OFF_QA, nx, s_full);
-        }
+        issue_grad(C_DV, c_s(j), Lay::OFF_DO, st, 1, false, &do_empty[st]);
+        if (!kTwoS && j + 1 < n_it && !(ok = next_scores())) break;
         if (!(ok = warp_wait(ds_full, j & 1, wc))) break;
         tc_fence_after();
         issue_grad(C_DK, C_DP, Lay::OFF_Q, st, 0, j == 0, nullptr);
@@ -445,7 +453,7 @@ __device__ __forceinline__ void key_tile(const CUtensorMap& tm_k, const CUtensor
     const int wl = warp & 3, half = warp >> 2;
     const int r = wl * 32 + lane;        // key row within the tile, TMEM lane
     const uint32_t at = tmem + (uint32_t(wl * 32) << 16);
-    const uint32_t s_col = at + C_S + 64 * half, dp_col = at + C_DP + 64 * half;
+    const uint32_t dp_col = at + C_DP + 64 * half;
     const int kb = (wl * 32) / BLK;      // key block within the tile (warp-uniform)
     bool ok = true;
     // The two 32-column groups' entries of step j + 1 are fetched in step j.
@@ -462,6 +470,7 @@ __device__ __forceinline__ void key_tile(const CUtensorMap& tm_k, const CUtensor
         next[g] = idx < n_ent ? __ldg(list.entry + e0 + idx) : 0;
         on[g] = ((ent[g] >> 16) >> kb) & 1;
       }
+      const uint32_t s_col = at + c_s(j) + 64 * half;
       if (!(ok = warp_wait(s_full, j & 1, wc))) break;
       tc_fence_after();
       // Two groups of 32 columns, the second loaded and the first stored
