@@ -315,8 +315,9 @@ def import_pattern(row_ptr, col_idx, B, H, n_blocks, block, retained_fx=None, to
                    device=None, stream=None):
     """A Pattern from a stored host CSR (e.g. Pattern.export('cpu') of an
     earlier selection). Arrays are converted to contiguous host int32/int64."""
-    device = torch.device("cuda", torch.cuda.current_device()) if device is None \
-        else torch.device(device)
+    device = torch.device("cuda" if device is None else device)
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
     host = lambda t, dt: None if t is None else \
         torch.as_tensor(t).to("cpu", dtype=dt).contiguous()
     rp, ci = host(row_ptr, torch.int32), host(col_idx, torch.int32)

@@ -127,6 +127,9 @@ bool valid_rope(const void* const (&in)[3], void* const (&out)[3], int in_dtype,
   int64_t features = 0, tokens = 1;
   for (int a = 0; a < s->n_axes; ++a) {
     if (s->dim[a] < 2 || s->dim[a] % 2 || s->dim[a] > d || !std::isfinite(s->scale[a])) return false;
+    // The axis's fastest and slowest pair.
+    const double slow = s->scale[a] * std::pow(s->theta, 2.0 / s->dim[a] - 1.0);
+    if (!std::isfinite(slow * 0x1p33) || !std::isfinite(s->scale[a] * 0x1p33)) return false;
     features += s->dim[a];
     if (s->grid[a] < 0) return false;
     tokens = std::min<int64_t>(tokens * s->grid[a], int64_t(1) << 31);
@@ -381,6 +384,11 @@ int losa_pattern_prepare_bwd(losa_pattern* p, void* stream) {
   if (p->key_mem) return LOSA_OK;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev != p->device) return LOSA_ERR_ARG;
+  // It allocates and synchronises, which would end a capture with an error.
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &capture) != cudaSuccess)
+    return LOSA_ERR_CUDA;
+  if (capture != cudaStreamCaptureStatusNone) return LOSA_ERR_ARG;
   return build_key_lists(p, static_cast<cudaStream_t>(stream));
 }
 
@@ -428,6 +436,13 @@ int losa_sparse_attn_bwd(const void* q, const void* k, const void* v, int in_dty
                         static_cast<const void*>(dk), static_cast<const void*>(dv),
                         static_cast<const void*>(workspace)})
     if (!aligned16(x)) return LOSA_ERR_ARG;
+  const void* const in[] = {q, k, v, o, lse, d_o, workspace};
+  void* const out[] = {dq, dk, dv};
+  for (int i = 0; i < 3; ++i) {
+    for (const void* x : in)
+      if (x == out[i]) return LOSA_ERR_ARG;
+    if (out[i] == out[(i + 1) % 3]) return LOSA_ERR_ARG;
+  }
   if (workspace_bytes < losa_sparse_attn_bwd_workspace(p, in_dtype, do_dtype, d))
     return LOSA_ERR_ARG;
   if (!is_sm100()) return LOSA_ERR_UNSUPPORTED;

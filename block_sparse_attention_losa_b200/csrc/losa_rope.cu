@@ -345,7 +345,7 @@ cudaError_t launch_rope(const RopeCall& c, cudaStream_t stream) {
   // absent axis has extent 1 and its position is never used.
   int ext[3] = {1, 1, 1};
   for (int a = 0; a < s.n_axes; ++a) {
-    ext[a] = s.grid[a];
+    ext[a] = std::max(1, s.grid[a]);  // 0: text alone, or positions listed
     p.start[a] = s.start[a];
   }
   p.grid_h = ext[1];

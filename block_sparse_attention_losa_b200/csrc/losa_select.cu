@@ -673,6 +673,15 @@ int build_key_lists(losa_pattern* p, cudaStream_t stream) {
     return code;
   };
   if (!mem || !scratch) return fail(LOSA_ERR_NOMEM);
+  if (stream != p->stream) {
+    // The pattern's own lists may still be under way on its stream.
+    cudaEvent_t built = nullptr;
+    const bool ok = cudaEventCreateWithFlags(&built, cudaEventDisableTiming) == cudaSuccess &&
+                    cudaEventRecord(built, p->stream) == cudaSuccess &&
+                    cudaStreamWaitEvent(stream, built, 0) == cudaSuccess;
+    if (built) cudaEventDestroy(built);
+    if (!ok) return fail(LOSA_ERR_CUDA);
+  }
   auto* ptr = reinterpret_cast<int32_t*>(mem);
   auto* order = reinterpret_cast<int32_t*>(mem + o_ord);
   auto* entry = reinterpret_cast<int32_t*>(mem + o_ent);

@@ -25,6 +25,11 @@
  *                     recomputed, the indices are not).
  *   losa_free         releases a pattern.
  *
+ * Around them, for training and for models' own layouts: losa_sparse_attn_bwd
+ * (gradients over the frozen pattern) and losa_rope_pack / losa_rope_unpack
+ * (rotary positions of a token grid, and the change between token-major
+ * projections and the layout below).
+ *
  * Conventions shared by every call:
  *   - Tensors are caller-owned DEVICE memory on the current CUDA device,
  *     contiguous, row-major. Q, K, V, O are [B, H, L_pad, d]; lse is
@@ -252,11 +257,13 @@ int losa_sparse_attn(const void* q, const void* k, const void* v, int in_dtype, 
  * every block; the masses carry no gradient). It walks the pattern by query
  * block and by key block, so losa_pattern_prepare_bwd has to be called once
  * on a pattern before: it builds the lists by key, allocates them from the
- * library's pool and synchronises `stream` once, so that they can then be
- * used on any stream. A second call does nothing. Not for use while another
- * thread uses the pattern, nor during stream capture.
- *   Returns LOSA_ERR_ARG for a null pattern or a current device other than
- *   the one the pattern was built on, LOSA_ERR_NOMEM, LOSA_ERR_CUDA.
+ * library's pool and synchronises `stream` once (which it first orders after
+ * the pattern's own stream), so that they can then be used on any stream. A
+ * second call does nothing. Not for use while another thread uses the
+ * pattern.
+ *   Returns LOSA_ERR_ARG for a null pattern, a current device other than the
+ *   one the pattern was built on or a stream that is being captured,
+ *   LOSA_ERR_NOMEM, LOSA_ERR_CUDA.
  */
 int losa_pattern_prepare_bwd(losa_pattern* p, void* stream);
 
@@ -288,8 +295,10 @@ int losa_pattern_export_bwd(const losa_pattern* p, int64_t* entries, int32_t* ke
  *   workspace at least losa_sparse_attn_bwd_workspace(...) bytes of device
  *             memory, 16-byte aligned, the call's own until it has run: calls
  *             or captured graphs that may run at the same time need one each.
- *   Rows >= L of every input are not used, whatever they hold. No output may
- *   overlap an input, the workspace or another output.
+ *   Rows >= L of every input are not used, whatever they hold. Values of the
+ *   other rows must be finite: as in the forward call, a tile's masked pairs
+ *   take weight 0, and 0 times infinity or NaN is NaN. No output may overlap
+ *   an input, the workspace or another output (equal addresses are refused).
  *   bf16 q, k, v run on tensor cores: P and dS are rounded to bf16 as their
  *   operands (half a unit in the 8th bit each), as is a fp32 d_o; all sums
  *   are fp32. fp32 q, k, v run in fp32 throughout (no tf32 rounding). No
@@ -297,7 +306,7 @@ int losa_pattern_export_bwd(const losa_pattern* p, int64_t* entries, int32_t* ke
  *   Does not allocate or synchronise, so it can be captured in a CUDA graph.
  *   Returns LOSA_ERR_ARG for a null or misaligned pointer (16 bytes; lse 4),
  *   a bad dtype, shape or scale (as losa_sparse_attn), a pattern not
- *   prepared, a workspace too small, a current device other than the
+ *   prepared, a workspace too small, equal addresses, a current device other than the
  *   pattern's; LOSA_ERR_UNSUPPORTED, LOSA_ERR_CUDA.
  */
 int losa_sparse_attn_bwd(const void* q, const void* k, const void* v, int in_dtype,
@@ -353,7 +362,8 @@ typedef struct {
  *   without its output or the reverse, a dtype out of range, B, H, L < 1,
  *   L_pad < L, L_pad - L >= 128, d not in {64, 128}, B*H > 65535, a pointer
  *   not aligned to its elements, a stride < 0 or > 2^40 / extent, a spec out of the
- *   ranges above (theta and scale finite, theta > 0, n_text <= L);
+ *   ranges above (theta and scale finite, theta > 0, n_text <= L, every
+ *   frequency times 2^33 finite);
  *   LOSA_ERR_UNSUPPORTED, LOSA_ERR_CUDA.
  */
 int losa_rope_pack(const void* q, const void* k, const void* v, int in_dtype,

@@ -369,6 +369,23 @@ def test_two_streams_at_once(losa):
         assert all(torch.equal(x, y) for x, y in zip(w, g))
 
 
+def test_lists_by_key_on_another_stream_than_the_selection(losa):
+    """The lists by key built on a side stream right after a selection on the
+    default one, whose list writes may still be running."""
+    g = torch.Generator("cuda").manual_seed(1)
+    mass = torch.rand(1, 8, 512, 512, generator=g, device="cuda")
+    mass /= mass.sum(-1, keepdim=True)
+    want = losa.select(mass, 64, 0.9).prepare_backward().export_backward()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        pat = losa.select(mass, 64, 0.9).prepare_backward(stream=side)
+        got = pat.export_backward()
+        assert torch.equal(want["key_ptr"], got["key_ptr"])
+        assert torch.equal(want["key_entry"], got["key_entry"])
+        pat.close()
+
+
 def test_given_outputs_and_workspace(losa):
     B, H, d, L, block = 1, 2, 64, 200, 32
     mask = make_mask(2, 7, 0.5, torch.Generator().manual_seed(3))
@@ -405,8 +422,19 @@ def test_refusals(losa):
         a.update(change)
         with pytest.raises(losa.LosaError):
             losa.sparse_attn_bwd(**a)
+    for change in (dict(dq=q), dict(dv=do), dict(dq=o, dk=o), dict(dk=q, dv=k)):
+        a = dict(q=q, k=k, v=v, o=o, lse=lse, do=do, L=L, pattern=pat)
+        a.update(change)
+        with pytest.raises(losa.LosaError):
+            losa.sparse_attn_bwd(**a)
     fresh = losa.import_pattern(*(pat.export("cpu")[x] for x in ("row_ptr", "col_idx")), B, H, 7,
-                                block)
+                                block, device="cuda")
+    stream = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        with pytest.raises(losa.LosaError):
+            fresh.prepare_backward(stream=stream)
+        torch.zeros(1, device="cuda")  # the capture goes on
     with pytest.raises(losa.LosaError):  # not prepared
         losa.sparse_attn_bwd(q, k, v, o, lse, do, L, fresh)
     with pytest.raises(losa.LosaError):

@@ -140,6 +140,23 @@ def test_strides_and_listed_positions(losa, pairing, layout):
     assert ((back[1].cpu().double() - ref).abs() <= (8 * U + 4e-6) * size).all()
 
 
+def test_text_alone_and_single_tokens(losa):
+    """A sequence of text tokens only is moved, not turned; one token of a
+    later chunk turns by its own position."""
+    x = torch.randn(2, 5, 3, 64, device="cuda").bfloat16()
+    rope = losa.Rope((0, 3, 3), (16, 24, 24), n_text=5)
+    q, k, v = losa.rope_pack(x, x, x, 32, rope)
+    for y in (q, k, v):
+        assert torch.equal(y[:, :, :5].transpose(1, 2), x) and (y[:, :, 5:] == 0).all()
+    one = torch.randn(1, 1, 2, 128, device="cuda")
+    for pairing in ("interleaved", "halves"):
+        rope = losa.Rope((1, 1, 1), (44, 42, 42), start=(1234567, 9, 77), pairing=pairing)
+        y = losa.rope_pack(one, None, None, 32, rope)[0][:, :, :1].transpose(1, 2)
+        ref, size = turn64(one.cpu().double(), torch.tensor([[[1234567, 9, 77]]]), (44, 42, 42),
+                           1e4, (1.0,) * 3, 0, pairing, 1)
+        close(y, ref, size)
+
+
 def test_untouched_neighbours_and_infinities(losa):
     """A fused gradient's other columns stay as they are; features that no
     axis turns pass infinities and NaN through unchanged."""

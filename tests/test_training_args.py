@@ -52,6 +52,7 @@ BAD = [
     dict(spec=dict(theta=float("nan"))), dict(spec=dict(scale=(1.0, float("nan"), 1.0))),
     dict(spec=dict(n_text=-1)), dict(spec=dict(n_text=108)), dict(spec=dict(pairing=2)),
     dict(pos=FAKE, spec=dict(n_text=108)),
+    dict(spec=dict(theta=1e-320, scale=(1.0, 1e10, 1.0))), dict(spec=dict(scale=(1e305, 1.0, 1.0))),
 ]
 
 
