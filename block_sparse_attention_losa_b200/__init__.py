@@ -514,6 +514,19 @@ def _token_strides(tensors):
 _ptr = lambda t: None if t is None else t.data_ptr()
 
 
+def _empty_each(tensors, shape, dtype, device):
+    """A new tensor for each one given."""
+    out, first = [], None
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        first = torch.empty(shape, dtype=dtype, device=device) if first is None \
+            else torch.empty_like(first)
+        out.append(first)
+    return out
+
+
 def rope_pack(q, k, v, block, rope: Rope, positions=None, out_dtype=None, out=None, stream=None):
     """Turns q and k [B, L, H, d] (any strides, features adjacent) by their
     tokens' positions and lays q, k, v out as the attention calls take them:
@@ -530,9 +543,7 @@ def rope_pack(q, k, v, block, rope: Rope, positions=None, out_dtype=None, out=No
     pos = _check_positions(positions, B, L, rope, device)
     with _on(stream, device):
         if out is None:
-            out = tuple(None if t is None else
-                        torch.empty((B, H, Lp, d), device=device, dtype=dtype)
-                        for t in (q, k, v))
+            out = _empty_each((q, k, v), (B, H, Lp, d), dtype, device)
         else:
             y = _same("out", out)
             if [t is None for t in (q, k, v)] != [t is None for t in out]:
@@ -564,9 +575,7 @@ def rope_unpack(q, k, v, L, rope: Rope, positions=None, out_dtype=None, out=None
     pos = _check_positions(positions, B, L, rope, device)
     with _on(stream, device):
         if out is None:
-            out = tuple(None if t is None else
-                        torch.empty((B, L, H, d), device=device, dtype=dtype)
-                        for t in (q, k, v))
+            out = _empty_each((q, k, v), (B, L, H, d), dtype, device)
         else:
             y = _same("out", out)
             if [t is None for t in (q, k, v)] != [t is None for t in out]:

@@ -29,32 +29,26 @@ namespace {
 
 // ------------------------------------------------------------------ D
 
-// D_i = dO_i . O_i, one warp per row; rows of the padding get 0. The sum is
-// held in fp32. Where dO's type is not that of q, k and v, `copy` receives it
-// in theirs: a fp32 dO is rounded to bf16, as the tensor cores read it, before
-// D is formed, so that D cancels against the same dO that dP is made of; a
-// bf16 one is widened.
-template <int D>
-__device__ __forceinline__ void load_row(const void* base, bool bf16, size_t row, int lane,
-                                         float (&v)[D / 32]) {
-  if (bf16) {
-    const uint16_t* p = static_cast<const uint16_t*>(base) + row * D + lane * (D / 32);
-#pragma unroll
-    for (int e = 0; e < D / 32; e += 2) {
-      const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(p + e));
-      v[e] = __uint_as_float(u << 16);
-      v[e + 1] = __uint_as_float(u & 0xffff0000u);
-    }
-  } else {
-    const float* p = static_cast<const float*>(base) + row * D + lane * (D / 32);
-#pragma unroll
-    for (int e = 0; e < D / 32; e += 2) {
-      const float2 u = __ldg(reinterpret_cast<const float2*>(p + e));
-      v[e] = u.x;
-      v[e + 1] = u.y;
+// Eight features of a row, as loaded and in fp32.
+struct Eight {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const void* base, bool bf16, size_t at) {
+    if (bf16) {
+      a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
+    } else {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + at);
+      a = __ldg(p);
+      b = __ldg(p + 1);
     }
   }
-}
+  __device__ __forceinline__ void get(bool bf16, float (&v)[8]) const {
+    const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      v[e] = !bf16 ? __uint_as_float(u[e])
+                   : __uint_as_float(e & 1 ? u[e / 2] & 0xffff0000u : u[e / 2] << 16);
+  }
+};
 
 // Three bf16 terms whose sum is x to 24 bits, as the first columns of a
 // 16-column operand row (the other columns 0).
@@ -75,51 +69,74 @@ struct AugRows {
   float inv_scale;
 };
 
+// D_i = dO_i . O_i for all rows (0 in the padding), the sum in fp32. Where
+// dO's type is not that of q, k and v, `copy` receives it in theirs: a fp32 dO
+// is rounded to bf16, as the tensor cores read it, before D is formed, so that
+// D cancels against the same dO that dP is made of; a bf16 one is widened.
+// Bound: HBM. D / 8 lanes share a row, and a warp has four sets of rows in
+// flight (one row per warp at a time took 20 us at 75,776 rows of 64).
+constexpr int kDeltaSets = 4;
 template <int D>
 __global__ void __launch_bounds__(256)
     delta_kernel(const void* o, bool o_bf16, const void* d_o, bool do_bf16, int64_t rows,
                  int L, int L_pad, float* delta, void* copy, const AugRows aug) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (row >= rows) return;
-  float sum = 0.f;
-  if (row % L_pad < L) {
-    float a[D / 32], b[D / 32];
-    load_row<D>(o, o_bf16, row, lane, a);
-    load_row<D>(d_o, do_bf16, row, lane, b);
-    if (copy && do_bf16) {
-      float* w = static_cast<float*>(copy) + row * D + lane * (D / 32);
+  constexpr int LANES = D / 8, SET = 32 / LANES;  // lanes of a row, rows of a set
+  const int lane = threadIdx.x & 31, part = lane % LANES;
+  const int64_t row0 =
+      (int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5)) * (kDeltaSets * SET) + lane / LANES;
+  Eight a[kDeltaSets], b[kDeltaSets];
+  bool valid[kDeltaSets];
 #pragma unroll
-      for (int e = 0; e < D / 32; e += 2) *reinterpret_cast<float2*>(w + e) = make_float2(b[e], b[e + 1]);
-    } else if (copy) {
-      uint32_t* w = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(copy) + row * D +
-                                                lane * (D / 32));
-#pragma unroll
-      for (int e = 0; e < D / 32; e += 2) {
-        const uint32_t u = pack_bf16x2(b[e], b[e + 1]);
-        w[e / 2] = u;
-        b[e] = __uint_as_float(u << 16);
-        b[e + 1] = __uint_as_float(u & 0xffff0000u);
-      }
+  for (int s = 0; s < kDeltaSets; ++s) {
+    const int64_t row = row0 + s * SET;
+    valid[s] = row < rows && row % L_pad < L;
+    if (valid[s]) {
+      a[s].load(o, o_bf16, size_t(row) * D + part * 8);
+      b[s].load(d_o, do_bf16, size_t(row) * D + part * 8);
     }
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) sum = fmaf(a[e], b[e], sum);
   }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  if (lane == 0) delta[row] = sum;
-  if (aug.q && lane < 4) {
-    // Lanes 0, 1: the row's two halves of q's columns; 2, 3: of dO's. Padded
-    // rows get a score far below any other, so their weight is 0; values are
-    // kept inside bf16's range.
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (lane == 0) {
-      const float a = row % L_pad < L ? -aug.lse[row] * aug.inv_scale : -3e38f;
-      x = split3(fminf(fmaxf(a, -3e38f), 3e38f));
-    } else if (lane == 2) {
-      x = split3(fminf(fmaxf(-sum, -3e38f), 3e38f));
+  for (int s = 0; s < kDeltaSets; ++s) {
+    const int64_t row = row0 + s * SET;
+    float sum = 0.f;
+    if (valid[s]) {
+      float x[8], y[8];
+      a[s].get(o_bf16, x);
+      b[s].get(do_bf16, y);
+      if (copy) {
+        const size_t at = size_t(row) * D + part * 8;
+        if (do_bf16) {
+          float4* w = reinterpret_cast<float4*>(static_cast<float*>(copy) + at);
+          w[0] = make_float4(y[0], y[1], y[2], y[3]);
+          w[1] = make_float4(y[4], y[5], y[6], y[7]);
+        } else {
+          Eight r;
+          r.a = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                           pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(copy) + at) = r.a;
+          r.get(true, y);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fmaf(x[e], y[e], sum);
     }
-    (lane < 2 ? aug.q : aug.d_o)[(row >> 3) * 16 + (lane & 1) * 8 + (row & 7)] = x;
+#pragma unroll
+    for (int off = LANES / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (row >= rows) continue;
+    if (part == 0) delta[row] = sum;
+    if (aug.q && part < 4) {
+      // Parts 0, 1: the row's two halves of q's columns; 2, 3: of dO's. Padded
+      // rows get a score far below any other, so their weight is 0; values are
+      // kept inside bf16's range.
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (part == 0) {
+        const float t = valid[s] ? -aug.lse[row] * aug.inv_scale : -3e38f;
+        w = split3(fminf(fmaxf(t, -3e38f), 3e38f));
+      } else if (part == 2) {
+        w = split3(fminf(fmaxf(-sum, -3e38f), 3e38f));
+      }
+      (part < 2 ? aug.q : aug.d_o)[(row >> 3) * 16 + (part & 1) * 8 + (row & 7)] = w;
+    }
   }
 }
 
@@ -288,7 +305,7 @@ __device__ __forceinline__ void fma_tile(const FmaParams& p, FmaSmem<D>& sm, int
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     f32x2 s2[4][NI] = {}, d2[4][NI] = {};
-#pragma unroll 2
+#pragma unroll 4
     for (int c = 0; c < CH; ++c) {
       const int yc = (c ^ (si & 7)) * 4;
       float4 xv[4], yv[NI];
@@ -457,7 +474,8 @@ cudaError_t launch_backward(const BackwardCall& c, cudaStream_t stream) {
   if (c.in_bf16)
     aug = {reinterpret_cast<uint4*>(ws + at.q_aug), reinterpret_cast<uint4*>(ws + at.do_aug), c.lse,
            1.f / c.scale};
-  const unsigned grid = unsigned((rows + 7) / 8);
+  const int64_t per_cta = 8 * kDeltaSets * (256 / c.d);
+  const unsigned grid = unsigned((rows + per_cta - 1) / per_cta);
   (c.d == 64 ? delta_kernel<64> : delta_kernel<128>)<<<grid, 256, 0, stream>>>(
       c.o, c.o_bf16, c.d_o, c.do_bf16, rows, c.L, L_pad, delta, copy, aug);
   cudaError_t err = cudaGetLastError();
