@@ -208,7 +208,7 @@ template <int D> struct KeyLayout {
   static constexpr int OFF_DA = OFF_QA + NS * kAugBytes;
   static constexpr int OFF_ONE = OFF_DA + NS * kAugBytes;
   static constexpr int OFF_BAR = OFF_ONE + kAugBytes;
-  static constexpr int N_BARS = 4 * NS + 8;
+  static constexpr int N_BARS = 4 * NS + 9;
   static constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
   static constexpr int BYTES = OFF_MISC + 16;
   // 1 KB of slack for alignment; above 116 KB, so that one CTA runs per SM
@@ -257,8 +257,9 @@ __device__ __forceinline__ void key_tile(const CUtensorMap& tm_k, const CUtensor
   uint64_t* q_empty = q_full + NS;     // [NS]
   uint64_t* do_full = q_empty + NS;    // [NS]
   uint64_t* do_empty = do_full + NS;   // [NS]
-  uint64_t* kv_full = do_empty + NS;   // K and V
-  uint64_t* s_full = kv_full + 1;
+  uint64_t* k_full = do_empty + NS;
+  uint64_t* v_full = k_full + 1;
+  uint64_t* s_full = v_full + 1;
   uint64_t* dp_full = s_full + 1;
   uint64_t* p_full = dp_full + 1;  // [2] first, second 32 columns of each half
   uint64_t* ds_full = p_full + 2;
@@ -275,14 +276,45 @@ __device__ __forceinline__ void key_tile(const CUtensorMap& tm_k, const CUtensor
   const int n_ent = list.ptr[tile + 1] - e0;
   const int n_it = (n_ent + EPI - 1) / EPI;
 
-  if (threadIdx.x == 0) {
+  // Step j's rows: slots past the end of the list repeat its last entry; the
+  // softmax masks their columns.
+  auto load_step = [&](const CUtensorMap* map, const uint16_t* aug, uint64_t* full, int off,
+                       int off_aug, int st, const int (&row)[EPI]) {
+    mbar_arrive_expect_tx(full, Lay::TILE_BYTES + kAugBytes);
+#pragma unroll
+    for (int e = 0; e < EPI; ++e) {
+#pragma unroll
+      for (int s = 0; s < SLABS; ++s)
+        tma_load_3d(smem + off + st * Lay::TILE_BYTES + s * (kTile * 128) + e * (BLK * 128), map,
+                    full, s * 64, row[e], bh);
+      bulk_load(smem + off_aug + st * kAugBytes + e * (BLK * 32),
+                aug + (size_t(bh) * p.L_pad + row[e]) * 16, BLK * 32, full);
+    }
+  };
+  auto step_rows = [&](int j, int (&row)[EPI]) {
+#pragma unroll
+    for (int e = 0; e < EPI; ++e)
+      row[e] = (list.entry[e0 + min(j * EPI + e, n_ent - 1)] & 0xFFFF) * BLK;
+  };
+  auto load_own = [&](const CUtensorMap* map, uint64_t* full, int off) {
+    mbar_arrive_expect_tx(full, Lay::TILE_BYTES);
+#pragma unroll
+    for (int s = 0; s < SLABS; ++s)
+      tma_load_3d(smem + off + s * (kTile * 128), map, full, s * 64, kt * kTile, bh);
+  };
+
+  // The loading thread sets the barriers up and sends off what the first step
+  // needs before the CTA meets, so that the copies run under the rest of the
+  // set-up.
+  if (warp == 8 && lane == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&q_full[s], 1);
       mbar_init(&q_empty[s], 1);
       mbar_init(&do_full[s], 1);
       mbar_init(&do_empty[s], 1);
     }
-    mbar_init(kv_full, 1);
+    mbar_init(k_full, 1);
+    mbar_init(v_full, 1);
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
     mbar_init(&p_full[0], 8);
@@ -292,6 +324,15 @@ __device__ __forceinline__ void key_tile(const CUtensorMap& tm_k, const CUtensor
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    fence_proxy_async_smem();
+    if (n_it > 0) {
+      int row[EPI];
+      load_own(&tm_k, k_full, Lay::OFF_K);
+      step_rows(0, row);
+      load_step(&tm_q, p.q_aug, &q_full[0], Lay::OFF_Q, Lay::OFF_QA, 0, row);
+      load_own(&tm_v, v_full, Lay::OFF_V);
+      load_step(&tm_do, p.do_aug, &do_full[0], Lay::OFF_DO, Lay::OFF_DA, 0, row);
+    }
   }
   // The ones: columns 0 to 2 of every row.
   for (int i = threadIdx.x; i < kAugBytes / 16; i += kBwdThreads) {
@@ -312,50 +353,24 @@ __device__ __forceinline__ void key_tile(const CUtensorMap& tm_k, const CUtensor
   if (warp == 8) {
     // ================================================================ producer
     if (lane == 0 && n_it > 0) {
-      tma_prefetch_map(&tm_k);
-      tma_prefetch_map(&tm_v);
-      tma_prefetch_map(&tm_q);
-      tma_prefetch_map(&tm_do);
-      mbar_arrive_expect_tx(kv_full, 2 * Lay::TILE_BYTES);
-#pragma unroll
-      for (int s = 0; s < SLABS; ++s) {
-        tma_load_3d(smem + Lay::OFF_K + s * (kTile * 128), &tm_k, kv_full, s * 64, kt * kTile, bh);
-        tma_load_3d(smem + Lay::OFF_V + s * (kTile * 128), &tm_v, kv_full, s * 64, kt * kTile, bh);
-      }
       bool ok = true;
-      int loaded_q = 0, loaded_do = 0;
-      for (int j = 0; ok && j < n_it; ++j) {
+      int loaded_q = 1, loaded_do = 1;
+      for (int j = 1; ok && j < n_it; ++j) {
         const int st = j % NS;
         const uint32_t parity = ((j / NS) & 1) ^ 1;
-        // Slots past the end of the list repeat its last entry; the softmax
-        // masks their columns.
         int row[EPI];
-#pragma unroll
-        for (int e = 0; e < EPI; ++e)
-          row[e] = (list.entry[e0 + min(j * EPI + e, n_ent - 1)] & 0xFFFF) * BLK;
-        auto load = [&](const CUtensorMap* map, const uint16_t* aug, uint64_t* full, int off,
-                        int off_aug) {
-          mbar_arrive_expect_tx(full, Lay::TILE_BYTES + kAugBytes);
-#pragma unroll
-          for (int e = 0; e < EPI; ++e) {
-#pragma unroll
-            for (int s = 0; s < SLABS; ++s)
-              tma_load_3d(smem + off + st * Lay::TILE_BYTES + s * (kTile * 128) + e * (BLK * 128),
-                          map, full, s * 64, row[e], bh);
-            bulk_load(smem + off_aug + st * kAugBytes + e * (BLK * 32),
-                      aug + (size_t(bh) * p.L_pad + row[e]) * 16, BLK * 32, full);
-          }
-        };
+        step_rows(j, row);
         if (!(ok = mbar_wait(&q_empty[st], parity, wc))) break;
-        load(&tm_q, p.q_aug, &q_full[st], Lay::OFF_Q, Lay::OFF_QA);
+        load_step(&tm_q, p.q_aug, &q_full[st], Lay::OFF_Q, Lay::OFF_QA, st, row);
         ++loaded_q;
         if (!(ok = mbar_wait(&do_empty[st], parity, wc))) break;
-        load(&tm_do, p.do_aug, &do_full[st], Lay::OFF_DO, Lay::OFF_DA);
+        load_step(&tm_do, p.do_aug, &do_full[st], Lay::OFF_DO, Lay::OFF_DA, st, row);
         ++loaded_do;
       }
       if (!ok) {
         // Aborted: let the copies in flight land before the CTA ends.
-        mbar_wait_drain(kv_full, 0);
+        mbar_wait_drain(k_full, 0);
+        mbar_wait_drain(v_full, 0);
         for (int i = max(loaded_q - NS, 0); i < loaded_q; ++i)
           mbar_wait_drain(&q_full[i % NS], (i / NS) & 1);
         for (int i = max(loaded_do - NS, 0); i < loaded_do; ++i)
@@ -405,11 +420,11 @@ __device__ __forceinline__ void key_tile(const CUtensorMap& tm_k, const CUtensor
         }
         __syncwarp();
       };
-      bool ok = warp_wait(kv_full, 0, wc) && warp_wait(&q_full[0], 0, wc);
+      bool ok = warp_wait(k_full, 0, wc) && warp_wait(&q_full[0], 0, wc);
       if (ok) {
         tc_fence_after();
         issue_scores(c_s(0), Lay::OFF_K, Lay::OFF_Q, Lay::OFF_QA, 0, s_full);
-        ok = warp_wait(&do_full[0], 0, wc);
+        ok = warp_wait(v_full, 0, wc) && warp_wait(&do_full[0], 0, wc);
       }
       if (ok) {
         tc_fence_after();
@@ -606,7 +621,24 @@ __device__ __forceinline__ void query_tile(const CUtensorMap& tm_k, const CUtens
   const int n_ent = list.ptr[tile + 1] - e0;  // at least 1: every query block keeps one
   const int n_it = (n_ent + EPI - 1) / EPI;
 
-  if (threadIdx.x == 0) {
+  auto load_step = [&](const CUtensorMap* map, uint64_t* full, int off, int st,
+                       const int (&row)[EPI]) {
+    mbar_arrive_expect_tx(full, Lay::TILE_BYTES);
+#pragma unroll
+    for (int e = 0; e < EPI; ++e)
+#pragma unroll
+      for (int s = 0; s < SLABS; ++s)
+        tma_load_3d(smem + off + st * Lay::TILE_BYTES + s * (kTile * 128) + e * (BLK * 128), map,
+                    full, s * 64, row[e], bh);
+  };
+  auto step_rows = [&](int j, int (&row)[EPI]) {
+#pragma unroll
+    for (int e = 0; e < EPI; ++e)
+      row[e] = (list.entry[e0 + min(j * EPI + e, n_ent - 1)] & 0xFFFF) * BLK;
+  };
+
+  // First copies before the CTA meets, as in key_tile.
+  if (warp == 8 && lane == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
@@ -623,6 +655,24 @@ __device__ __forceinline__ void query_tile(const CUtensorMap& tm_k, const CUtens
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    fence_proxy_async_smem();
+    int row[EPI];
+    step_rows(0, row);
+    load_step(&tm_k, &k_full[0], Lay::OFF_K, 0, row);
+    load_step(&tm_v, &v_full[0], Lay::OFF_V, 0, row);
+  }
+  // The score warps' own rows, on their way to tensor memory: warps 0-3 Q,
+  // warps 4-7 dO; zero past L.
+  uint4 own[D / 8];
+  if (warp < 8) {
+    const int row = qt * kTile + (warp & 3) * 32 + lane;
+    const uint16_t* src =
+        static_cast<const uint16_t*>(warp >> 2 ? p.d_o : p.q) + (size_t(bh) * p.L_pad + row) * D;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      own[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < p.L) own[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+    }
   }
   if (warp == 9) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
@@ -636,31 +686,18 @@ __device__ __forceinline__ void query_tile(const CUtensorMap& tm_k, const CUtens
   if (warp == 8) {
     // ================================================================ producer
     if (lane == 0) {
-      tma_prefetch_map(&tm_k);
-      tma_prefetch_map(&tm_v);
       bool ok = true;
-      int loaded_k = 0, loaded_v = 0;
-      for (int j = 0; ok && j < n_it; ++j) {
+      int loaded_k = 1, loaded_v = 1;
+      for (int j = 1; ok && j < n_it; ++j) {
         const int st = j % NS;
         const uint32_t parity = ((j / NS) & 1) ^ 1;
         int row[EPI];
-#pragma unroll
-        for (int e = 0; e < EPI; ++e)
-          row[e] = (list.entry[e0 + min(j * EPI + e, n_ent - 1)] & 0xFFFF) * BLK;
-        auto load = [&](const CUtensorMap* map, uint64_t* full, int off) {
-          mbar_arrive_expect_tx(full, Lay::TILE_BYTES);
-#pragma unroll
-          for (int e = 0; e < EPI; ++e)
-#pragma unroll
-            for (int s = 0; s < SLABS; ++s)
-              tma_load_3d(smem + off + st * Lay::TILE_BYTES + s * (kTile * 128) + e * (BLK * 128),
-                          map, full, s * 64, row[e], bh);
-        };
+        step_rows(j, row);
         if (!(ok = mbar_wait(&k_empty[st], parity, wc))) break;
-        load(&tm_k, &k_full[st], Lay::OFF_K);
+        load_step(&tm_k, &k_full[st], Lay::OFF_K, st, row);
         ++loaded_k;
         if (!(ok = mbar_wait(&v_empty[st], parity, wc))) break;
-        load(&tm_v, &v_full[st], Lay::OFF_V);
+        load_step(&tm_v, &v_full[st], Lay::OFF_V, st, row);
         ++loaded_v;
       }
       if (!ok) {
@@ -747,23 +784,18 @@ __device__ __forceinline__ void query_tile(const CUtensorMap& tm_k, const CUtens
     const uint32_t at = tmem + (uint32_t(wl * 32) << 16);
     const uint32_t s_col = at + C_S + 64 * half, dp_col = at + C_DP + 64 * half;
     const int qb = (wl * 32) / BLK;
-    // Own rows to tensor memory: warps 0-3 Q, warps 4-7 dO; zero past L.
-    {
-      const uint16_t* src = static_cast<const uint16_t*>(half ? p.d_o : p.q) + flat * D;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t u[16];
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t u[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (valid) x = __ldg(reinterpret_cast<const uint4*>(src + c * 32 + i * 8));
-          u[4 * i] = x.x, u[4 * i + 1] = x.y, u[4 * i + 2] = x.z, u[4 * i + 3] = x.w;
-        }
-        tmem_st16(at + (half ? C_DO : C_Q) + 16 * c, u);
+      for (int i = 0; i < 4; ++i) {
+        const uint4 x = own[4 * c + i];
+        u[4 * i] = x.x, u[4 * i + 1] = x.y, u[4 * i + 2] = x.z, u[4 * i + 3] = x.w;
       }
-      tmem_st_wait();
-      warp_arrive(own_full, lane);
+      tmem_st16(at + (half ? C_DO : C_Q) + 16 * c, u);
     }
+    tmem_st_wait();
+    warp_arrive(own_full, lane);
     const float NEG_INF = -__int_as_float(0x7f800000);
     const float shift = valid ? -p.lse[flat] * 1.4426950408889634f : NEG_INF;
     const float delta = valid ? p.delta[flat] : 0.f;
