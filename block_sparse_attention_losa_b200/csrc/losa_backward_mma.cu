@@ -208,7 +208,7 @@ template <int D> struct KeyLayout {
   static constexpr int OFF_DA = OFF_QA + NS * kAugBytes;
   static constexpr int OFF_ONE = OFF_DA + NS * kAugBytes;
   static constexpr int OFF_BAR = OFF_ONE + kAugBytes;
-  static constexpr int N_BARS = 4 * NS + 9;
+  static constexpr int N_BARS = 4 * NS + 12;
   static constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
   static constexpr int BYTES = OFF_MISC + 16;
   // 1 KB of slack for alignment; above 116 KB, so that one CTA runs per SM
@@ -245,7 +245,10 @@ __device__ __forceinline__ void key_tile(const CUtensorMap& tm_k, const CUtensor
   // S and P of step j: at D = 64 two buffers fit, and S(j+1) is formed while
   // step j's are in use.
   constexpr bool kTwoS = D == 64;
-  auto c_s = [](int j) -> uint32_t { return kTwoS && (j & 1) ? 384u : 0u; };
+  auto buffer = [](int j) -> int { return kTwoS ? j & 1 : 0; };
+  auto c_s = [&](int j) -> uint32_t { return 384u * buffer(j); };
+  // Parity of step j's use of its buffer's barriers.
+  auto use = [](int j) -> uint32_t { return (kTwoS ? j >> 1 : j) & 1; };
   constexpr uint32_t IDESC_S = idesc_bf16_f32(kTile, kTile, false, false);
   constexpr uint32_t IDESC_G = idesc_bf16_f32(kTile, D, false, true);
 
@@ -259,10 +262,14 @@ __device__ __forceinline__ void key_tile(const CUtensorMap& tm_k, const CUtensor
   uint64_t* do_empty = do_full + NS;   // [NS]
   uint64_t* k_full = do_empty + NS;
   uint64_t* v_full = k_full + 1;
-  uint64_t* s_full = v_full + 1;
-  uint64_t* dp_full = s_full + 1;
-  uint64_t* p_full = dp_full + 1;  // [2] first, second 32 columns of each half
-  uint64_t* ds_full = p_full + 2;
+  // Scores and weights, one set per buffer of S: with two, S(j+1) may be
+  // complete before a slow warp has seen S(j), and a fast warp may deliver
+  // P(j+1) before a slow one P(j). A buffer's next use comes after all warps'
+  // last one, whose P the MMA warp has waited for.
+  uint64_t* s_full = v_full + 1;   // [2]
+  uint64_t* p_full = s_full + 2;   // [2][2] first, second 32 columns of each half
+  uint64_t* dp_full = p_full + 4;
+  uint64_t* ds_full = dp_full + 1;
   uint64_t* acc_full = ds_full + 1;
   uint64_t* drain_bar = acc_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::OFF_MISC);
@@ -315,10 +322,10 @@ __device__ __forceinline__ void key_tile(const CUtensorMap& tm_k, const CUtensor
     }
     mbar_init(k_full, 1);
     mbar_init(v_full, 1);
-    mbar_init(s_full, 1);
+    mbar_init(&s_full[0], 1);
+    mbar_init(&s_full[1], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], 8);
     mbar_init(dp_full, 1);
-    mbar_init(&p_full[0], 8);
-    mbar_init(&p_full[1], 8);
     mbar_init(ds_full, 8);
     mbar_init(acc_full, 1);
     mbar_init(drain_bar, 1);
@@ -423,7 +430,7 @@ __device__ __forceinline__ void key_tile(const CUtensorMap& tm_k, const CUtensor
       bool ok = warp_wait(k_full, 0, wc) && warp_wait(&q_full[0], 0, wc);
       if (ok) {
         tc_fence_after();
-        issue_scores(c_s(0), Lay::OFF_K, Lay::OFF_Q, Lay::OFF_QA, 0, s_full);
+        issue_scores(c_s(0), Lay::OFF_K, Lay::OFF_Q, Lay::OFF_QA, 0, &s_full[0]);
         ok = warp_wait(v_full, 0, wc) && warp_wait(&do_full[0], 0, wc);
       }
       if (ok) {
@@ -436,14 +443,15 @@ __device__ __forceinline__ void key_tile(const CUtensorMap& tm_k, const CUtensor
         auto next_scores = [&]() -> bool {
           if (!warp_wait(&q_full[nx], nx_parity, wc)) return false;
           tc_fence_after();
-          issue_scores(c_s(j + 1), Lay::OFF_K, Lay::OFF_Q, Lay::OFF_QA, nx, s_full);
+          issue_scores(c_s(j + 1), Lay::OFF_K, Lay::OFF_Q, Lay::OFF_QA, nx,
+                       &s_full[buffer(j + 1)]);
           return true;
         };
         if (kTwoS && j + 1 < n_it && !(ok = next_scores())) break;
-        if (!(ok = warp_wait(&p_full[0], j & 1, wc))) break;
+        if (!(ok = warp_wait(&p_full[2 * buffer(j)], use(j), wc))) break;
         tc_fence_after();
         issue_grad(C_DV, c_s(j), Lay::OFF_DO, st, 0, j == 0, nullptr);
-        if (!(ok = warp_wait(&p_full[1], j & 1, wc))) break;
+        if (!(ok = warp_wait(&p_full[2 * buffer(j) + 1], use(j), wc))) break;
         tc_fence_after();
         issue_grad(C_DV, c_s(j), Lay::OFF_DO, st, 1, false, &do_empty[st]);
         if (!kTwoS && j + 1 < n_it && !(ok = next_scores())) break;
@@ -486,7 +494,7 @@ __device__ __forceinline__ void key_tile(const CUtensorMap& tm_k, const CUtensor
         on[g] = ((ent[g] >> 16) >> kb) & 1;
       }
       const uint32_t s_col = at + c_s(j) + 64 * half;
-      if (!(ok = warp_wait(s_full, j & 1, wc))) break;
+      if (!(ok = warp_wait(&s_full[buffer(j)], use(j), wc))) break;
       tc_fence_after();
       // Two groups of 32 columns, the second loaded and the first stored
       // under the other's arithmetic; the first can feed dV at once. A group
@@ -504,14 +512,14 @@ __device__ __forceinline__ void key_tile(const CUtensorMap& tm_k, const CUtensor
       tmem_st_bf16(s_col, w0);
       tmem_ld_wait();
       tmem_st_wait();
-      warp_arrive(&p_full[0], lane);
+      warp_arrive(&p_full[2 * buffer(j)], lane);
       if (on[1])
         exp2_scaled(w1, p.scale_log2);
       else
         zero32(w1);
       tmem_st_bf16(s_col + 16, w1);
       tmem_st_wait();
-      warp_arrive(&p_full[1], lane);
+      warp_arrive(&p_full[2 * buffer(j) + 1], lane);
       if (!(ok = warp_wait(dp_full, j & 1, wc))) break;
       tc_fence_after();
       float y0[32], y1[32];

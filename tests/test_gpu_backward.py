@@ -369,6 +369,29 @@ def test_two_streams_at_once(losa):
         assert all(torch.equal(x, y) for x, y in zip(w, g))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("flip", [False, True])
+def test_uneven_warps(losa, d, flip):
+    """Blocks of 32 in a checkerboard in which every second pair of a step's
+    four blocks is kept by one block of a tile only: some warps of a tile skip
+    all their arithmetic, others none, over many steps, so that they drift as
+    far apart as the kernel lets them."""
+    B, H, L, block = 1, 3, 1984, 32
+    n = L // block
+    i, j = torch.arange(n)[:, None], torch.arange(n)[None, :]
+    mask = torch.where(j % 4 < 2, i % 4 == 3, i % 4 != 3)
+    if flip:
+        mask = mask.T | (i == j)
+    mask = mask | (j == i // 4 * 4)
+    mask = mask[None].repeat(H, 1, 1)
+    pat = pattern_of(losa, mask, B, H, block)
+    args, ref, tol = inputs(B, H, L, L, d, BF, F32, BF, mask, block, 41)
+    for _ in range(3):
+        got = losa.sparse_attn_bwd(*args, L, pat)
+        losa.check_status()
+        close(got, ref, tol, L)
+
+
 def test_lists_by_key_on_another_stream_than_the_selection(losa):
     """The lists by key built on a side stream right after a selection on the
     default one, whose list writes may still be running."""
