@@ -208,35 +208,50 @@ __global__ void __launch_bounds__(kRopeThreads)
   };
   load(0, h0);
 
-  // Adjacent: cs[e], sn[e] of the pair (2e, 2e + 1). By halves, per feature:
-  // y[e] = x[e] cs[e] + partner sn[e], the partner at word from[e] of the
-  // exchange (feature 8 g + e of the row at word 32 e + g).
+  // The thread's four pairs in feature order. Adjacent: cs[e], sn[e] of the
+  // pair (2e, 2e + 1). By halves, per feature: y[e] = x[e] cs[e] + partner
+  // sn[e], the partner at word from[e] of the exchange (feature 8 g + e of the
+  // row at word 32 e + g); the pairs' values come from the threads of the row
+  // that computed them.
   constexpr int NA = kHalves ? 8 : 4;
   float cs[NA], sn[NA];
   int from[kHalves ? 8 : 1];
+  __shared__ float2 turned[kHalves ? kRopeThreads * 4 : 1];
   int n_turn = 0;  // features of this thread that turn
   if (valid) {
     const Place x = place_of(p, b, l);
     if (!x.text) n_turn = min(max(p.n_rot - f0, 0), 8);
 #pragma unroll
-    for (int e = 0; e < NA; ++e) {
+    for (int e = 0; e < 4; ++e) {
+      float c = 1.f, s = 0.f;
+      if (2 * e < n_turn) turn_of(p, x, f0 / 2 + e, c, s);
+      if (kUnpack) s = -s;
+      if constexpr (kHalves) {
+        turned[threadIdx.x * 4 + e] = make_float2(c, s);
+      } else {
+        cs[e] = c;
+        sn[e] = s;
+      }
+    }
+  }
+  if constexpr (kHalves) {
+    __syncwarp();
+    const float2* row = turned + (threadIdx.x - threadIdx.x % groups) * 4;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
       cs[e] = 1.f;
       sn[e] = 0.f;
-      const int f = kHalves ? f0 + e : f0 + 2 * e;
-      if constexpr (kHalves) from[e] = 32 * e + lane;
-      if (f - f0 >= n_turn) continue;
-      if constexpr (kHalves) {
-        const int axis = (p.n_axes > 2 && f >= p.base[2]) ? 2 : (p.n_axes > 1 && f >= p.base[1]);
-        const int half = p.half[axis], i = f - p.base[axis];
-        const bool second = i >= half;
-        turn_of(p, x, p.base[axis] / 2 + (second ? i - half : i), cs[e], sn[e]);
-        if (kUnpack == second) sn[e] = -sn[e];  // minus sin of the first feature
-        const int other = second ? f - half : f + half;
-        from[e] = 32 * (other & 7) + (lane & ~(groups - 1)) + (other >> 3);
-      } else {
-        turn_of(p, x, f / 2, cs[e], sn[e]);
-        if (kUnpack) sn[e] = -sn[e];
-      }
+      from[e] = 32 * e + lane;
+      const int f = f0 + e;
+      if (e >= n_turn) continue;
+      const int axis = (p.n_axes > 2 && f >= p.base[2]) ? 2 : (p.n_axes > 1 && f >= p.base[1]);
+      const int half = p.half[axis], i = f - p.base[axis];
+      const bool second = i >= half;
+      const float2 t = row[p.base[axis] / 2 + (second ? i - half : i)];
+      cs[e] = t.x;
+      sn[e] = second ? t.y : -t.y;  // minus sin of the first feature
+      const int other = second ? f - half : f + half;
+      from[e] = 32 * (other & 7) + (lane & ~(groups - 1)) + (other >> 3);
     }
   }
 
