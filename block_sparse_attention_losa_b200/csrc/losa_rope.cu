@@ -17,7 +17,7 @@
 // Measured on a B200 with cold caches, bf16, launch included: 105 us at the
 // Wan2.1-1.3B shape (12 heads, 32,760 tokens, d 128: 5.7 TB/s), 684 us at
 // the HunyuanVideo one (24 heads, 118,800 tokens: 6.4 TB/s, 0.99 of the
-// measured copy rate); by halves 116 us at the first. Tried and slower: 16
+// measured copy rate); by halves 110 us at the first. Tried and slower: 16
 // features a thread in two groups of 128 contiguous bytes a row (862 us at
 // the second; the rows' halves then move apart), two features a thread (250
 // us by halves at the first), and one loop over all tensors' heads with its
@@ -162,10 +162,13 @@ __device__ __forceinline__ void store_any(__nv_bfloat16* p, const float (&v)[8])
 // kUnpack: packed -> token-major by the negative angle. kHalves: pair i of an
 // axis is its features (i, i + dim/2) instead of (2i, 2i + 1). kVec: every
 // group of eight features is 16-byte aligned on both sides.
-template <typename TI, typename TO, bool kUnpack, bool kHalves, bool kVec>
+// kFew: the CTA has at most two heads, and the loads of all three tensors go
+// out together (with one head after another's three round trips to memory, a
+// single head of 118,800 tokens took 85 us, now 71, most of it angles).
+template <typename TI, typename TO, bool kUnpack, bool kHalves, bool kVec, bool kFew>
 __global__ void __launch_bounds__(kRopeThreads)
     rope_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int BATCH = 4;
+  constexpr int BATCH = kFew ? 2 : 4;
   const int groups = p.d / 8;
   const int f0 = 8 * (threadIdx.x % groups);
   const int lane = threadIdx.x & 31;
@@ -191,8 +194,8 @@ __global__ void __launch_bounds__(kRopeThreads)
   }  // by halves a warp's threads stay together for the exchange
 
   // Heads first .. first + BATCH - 1 of tensor t.
-  Raw<TI> raw[BATCH];
-  auto load = [&](int t, int first) {
+  Raw<TI> raws[kFew ? 3 : 1][BATCH];
+  auto load = [&](int t, int first, Raw<TI> (&raw)[BATCH]) {
     const TI* in = static_cast<const TI*>(p.in[t]) + f0 +
                    (kUnpack ? packed_at(p, b, l, first) : flat_at(p, t, b, l, first));
     const size_t step = kUnpack ? size_t(p.L_pad) * p.d : size_t(p.sh[t]);
@@ -206,7 +209,11 @@ __global__ void __launch_bounds__(kRopeThreads)
       }
     }
   };
-  load(0, h0);
+  load(0, h0, raws[0]);
+  if constexpr (kFew) {
+    if (p.n_tensors > 1) load(1, h0, raws[1]);
+    if (p.n_tensors > 2) load(2, h0, raws[2]);
+  }
 
   // The thread's four pairs in feature order. Adjacent: cs[e], sn[e] of the
   // pair (2e, 2e + 1). By halves, per feature: y[e] = x[e] cs[e] + partner
@@ -255,14 +262,15 @@ __global__ void __launch_bounds__(kRopeThreads)
     }
   }
 
-  __shared__ float exchange[kHalves ? kRopeThreads / 32 : 1][BATCH][kHalves ? 8 * 32 : 1];
+  __shared__ float exchange[kHalves ? kRopeThreads / 32 : 1][4][kHalves ? 8 * 32 : 1];
   const int warp = threadIdx.x >> 5;
 #pragma unroll
   for (int t = 0; t < 3; ++t) {
     if (t >= p.n_tensors) break;
     const size_t step = kUnpack ? size_t(p.sh[t]) : size_t(p.L_pad) * p.d;
     for (int first = h0; first < h1; first += BATCH) {
-      if (t > 0 || first > h0) load(t, first);
+      Raw<TI>(&raw)[BATCH] = raws[kFew ? t : 0];
+      if (!kFew && (t > 0 || first > h0)) load(t, first, raw);
       TO* out = static_cast<TO*>(p.out[t]) + f0 +
                 (kUnpack ? flat_at(p, t, b, l, first) : packed_at(p, b, l, first));
 #pragma unroll
@@ -272,7 +280,7 @@ __global__ void __launch_bounds__(kRopeThreads)
         raw[i].get(x);
         if (p.turns[t]) {
           if constexpr (kHalves) {
-            float* buf = exchange[warp][i];
+            float* buf = exchange[warp][kFew ? 2 * (t & 1) + i : i];
 #pragma unroll
             for (int e = 0; e < 8; ++e) buf[32 * e + lane] = x[e];
             __syncwarp();
@@ -310,10 +318,12 @@ bool multiple16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) =
 template <typename TI, typename TO>
 cudaError_t launch(const RopeParams& p, bool unpack, bool halves, bool vec, dim3 grid,
                    cudaStream_t stream) {
-#define LOSA_ROPE(U_, H_, V_)                                          \
-  if (unpack == U_ && halves == H_ && vec == V_) {                     \
-    rope_kernel<TI, TO, U_, H_, V_><<<grid, kRopeThreads, 0, stream>>>(p); \
-    return cudaGetLastError();                                         \
+#define LOSA_ROPE(U_, H_, V_)                                                   \
+  if (unpack == U_ && halves == H_ && vec == V_) {                              \
+    (p.head_step <= 2 ? rope_kernel<TI, TO, U_, H_, V_, true>                   \
+                      : rope_kernel<TI, TO, U_, H_, V_, false>)                 \
+        <<<grid, kRopeThreads, 0, stream>>>(p);                                 \
+    return cudaGetLastError();                                                  \
   }
   LOSA_ROPE(false, false, true)
   LOSA_ROPE(false, false, false)
