@@ -432,8 +432,9 @@ __global__ void __launch_bounds__(T, T == 128 ? 2 : 1) bwd_fma_kernel(const FmaP
 }
 
 template <int D, int T> cudaError_t run_fma(const FmaParams& p, cudaStream_t stream) {
-  const cudaError_t err = cudaFuncSetAttribute(
-      bwd_fma_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(FmaSmem<D>)));
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t err = allow_smem(reinterpret_cast<const void*>(bwd_fma_kernel<D, T>),
+                                     int(sizeof(FmaSmem<D>)), allowed);
   if (err != cudaSuccess) return err;
   bwd_fma_kernel<D, T><<<8u * unsigned(p.n_tiles), T, sizeof(FmaSmem<D>), stream>>>(p);
   return cudaGetLastError();

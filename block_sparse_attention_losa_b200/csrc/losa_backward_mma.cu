@@ -934,8 +934,8 @@ cudaError_t run_mma(const BackwardCall& c, const BackwardOperands& w, const BwdP
     return cudaErrorInvalidValue;
   auto kern = bwd_tiles_kernel<D, BLK, kOutBf16>;
   constexpr int smem = std::max(KeyLayout<D>::SMEM_ALLOC, QueryLayout<D>::SMEM_ALLOC);
-  const cudaError_t err =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t err = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed);
   if (err != cudaSuccess) return err;
   kern<<<2u * unsigned(p.n_tiles), kBwdThreads, smem, stream>>>(own_k, own_v, step_q, step_do,
                                                                step_k, step_v, p);

@@ -2,6 +2,7 @@
 // translation units (not part of the public ABI).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -51,6 +52,10 @@ struct NvtxRange {
 
 // True when the current device is an sm_100 part (the only target built).
 bool is_sm100();
+
+// Allows a kernel `bytes` of dynamic shared memory, once per device; `done`
+// is the kernel's own record (a bit per device).
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 
 // Device status word of the current device (lazily resolved per device).
 int* device_status_word();

@@ -379,9 +379,10 @@ cudaError_t launch_rope(const RopeCall& c, cudaStream_t stream) {
   for (int a = 0; a < s.n_axes; ++a) {
     p.base[a] = short(f);
     p.half[a] = short(s.dim[a] / 2);
+    const double step = -2.0 * std::log(s.theta) / s.dim[a];
     for (int i = 0; i < s.dim[a] / 2; ++i) {
       p.axis[f / 2 + i] = (unsigned char)a;
-      p.freq[f / 2 + i] = s.scale[a] * std::pow(s.theta, -2.0 * i / s.dim[a]) / (2.0 * M_PI);
+      p.freq[f / 2 + i] = s.scale[a] * std::exp(step * i) / (2.0 * M_PI);
     }
     f += s.dim[a];
   }
