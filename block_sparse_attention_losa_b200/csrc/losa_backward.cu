@@ -192,16 +192,19 @@ __device__ __forceinline__ void dot4(const float4& a, const float4& b, f32x2& ac
 // of keys (kKeys: dK and dV) or of queries (dQ) and walks those list entries
 // whose blocks meet, 64 rows of the other side at a time: two segments of 32
 // rows, the unit in which blocks of 32, 64 and 128 rows start and end.
-// Every product is fp32 FMA, and what bounds it is the reads of its operands
-// from shared memory (a 16-byte read of a warp takes two cycles of the SM's
-// shared memory even where its lanes ask for little), so few threads hold
-// large tiles. With T = 128:
+// Every product is fp32 FMA, bound by the FMA units and the reads of its
+// operands from shared memory. A 16-byte read of a warp takes two cycles of
+// shared memory where each lane wants what lane ^ 1 or each what lane ^ 2
+// wants, else four (measured, whatever the number of distinct addresses), so
+// bit 0 of a lane picks among own rows alone and bit 1 among the other
+// operand's alone (before: 3.0 a read, and 2.43 ms for the case below); and
+// few threads hold large tiles. With T = 128:
 //   scores: a warp has 16 x 32 of the 32 x 64, a thread 4 x 4 of it;
 //   gradients: a thread has 8 own rows x 8 features; the threads hold both
 //   products (keys) and, with what is left, parts of the step's rows, summed
 //   at the end.
-// 5,000 tokens, 8 heads, d 64, half the blocks kept: 2.47 ms, 26 TFLOP/s of
-// the five products that the gradient needs, 37 of the seven that run.
+// 5,000 tokens, 8 heads, d 64, half the blocks kept: 2.38 ms, 27 TFLOP/s of
+// the five products that the gradient needs, 38 of the seven that run.
 template <int D, int T, bool kKeys>
 __device__ __forceinline__ void fma_tile(const FmaParams& p, FmaSmem<D>& sm, int tile,
                                          int quarter) {
@@ -261,13 +264,14 @@ __device__ __forceinline__ void fma_tile(const FmaParams& p, FmaSmem<D>& sm, int
   fill(&sm.x2[0][0], kKeys ? p.v : p.d_o, own0, true);
 
   // Scores: the warp's 16 own rows and WARP_ROWS step rows, the thread's rows
-  // so + 4 a and si + 8 i.
-  const int so = 16 * (warp / (T / 64)) + (lane >> 3);
-  const int si = WARP_ROWS * (warp % (T / 64)) + (lane & 7);
+  // so + 4 a and si + 8 i, four own rows by bits 0 and 2 of the lane, eight
+  // step rows by the others.
+  const int so = 16 * (warp / (T / 64)) + (lane & 1) + 2 * (lane >> 2 & 1);
+  const int si = WARP_ROWS * (warp % (T / 64)) + (lane >> 1 & 1) + 2 * (lane >> 3);
   // Gradients: own rows go.. and chunks gc and gc + CH / 2, for the group's
   // product and part.
   const int group = tid / PER, within = tid % PER;
-  const int go = 8 * (within / (CH / 2)), gc = within % (CH / 2);
+  const int go = 8 * ((within & 1) + 2 * (within / CH)), gc = (within >> 1) % (CH / 2);
   const bool use_p = kKeys && (group & 1);
   const int gpart = kKeys ? group >> 1 : group;
   f32x2 acc[4][8] = {};  // pairs of own rows x features
