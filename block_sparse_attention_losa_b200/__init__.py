@@ -617,7 +617,8 @@ def layer_attn(q, k, v, rope: Rope, pattern: Pattern, positions=None, scale=None
         # O stays fp32 for the backward pass, whose D = dO . O cancels against
         # dP; the layer's output is rounded once.
         o, lse = sparse_attn(qp, kp, vp, L, pattern, scale=scale, stream=stream)
-        out = rope_unpack(None, None, o, L, rope, out_dtype=q.dtype, stream=stream)[2]
+        out = rope_unpack(None, None, o, L, rope, positions=positions, out_dtype=q.dtype,
+                          stream=stream)[2]
     return out, LayerState(qp, kp, vp, o, lse, L, rope, pattern, positions, scale)
 
 

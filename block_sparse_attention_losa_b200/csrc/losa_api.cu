@@ -132,6 +132,13 @@ bool valid_rope(const void* const (&in)[3], void* const (&out)[3], int in_dtype,
       reach += x.stride * (x.n - 1);
     }
   }
+  for (int t = 0; t < 3; ++t) {
+    if (!out[t]) continue;
+    for (const void* x : in)
+      if (x == out[t]) return false;
+    if (out[t] == out[(t + 1) % 3]) return false;
+  }
+  if (reinterpret_cast<uintptr_t>(positions) % sizeof(int32_t)) return false;
   if (s->n_axes < 1 || s->n_axes > 3 || s->n_text < 0 || s->n_text > L) return false;
   if (s->pairing != LOSA_ROPE_INTERLEAVED && s->pairing != LOSA_ROPE_HALVES) return false;
   if (!(std::isfinite(s->theta) && s->theta > 0.0)) return false;
@@ -447,6 +454,7 @@ int losa_sparse_attn_bwd(const void* q, const void* k, const void* v, int in_dty
                         static_cast<const void*>(dk), static_cast<const void*>(dv),
                         static_cast<const void*>(workspace)})
     if (!aligned16(x)) return LOSA_ERR_ARG;
+  if (reinterpret_cast<uintptr_t>(lse) % sizeof(float)) return LOSA_ERR_ARG;
   const void* const in[] = {q, k, v, o, lse, d_o, workspace};
   void* const out[] = {dq, dk, dv};
   for (int i = 0; i < 3; ++i) {

@@ -351,7 +351,7 @@ typedef struct {
  *             the three may be NULL together with its output.
  *   q_out, k_out, v_out  [B, H, L_pad, d] contiguous, out_dtype; q and k
  *             turned, v as it is; rows >= L are 0. They must not overlap the
- *             inputs.
+ *             inputs or each other (equal addresses are refused).
  *   positions [B, L, n_axes] int32 device, contiguous, or NULL: positions
  *             listed per token instead of spec's grid and start (scale still
  *             applies; the first n_text tokens are not turned).
@@ -359,7 +359,7 @@ typedef struct {
  *   values are turned in fp32 and rounded once.
  *   Neither allocates nor synchronises.
  *   Returns LOSA_ERR_ARG for: null spec, strides or all of q, k, v, an input
- *   without its output or the reverse, a dtype out of range, B, H, L < 1,
+ *   without its output or the reverse, equal addresses, a dtype out of range, B, H, L < 1,
  *   L_pad < L, L_pad - L >= 128, d not in {64, 128}, B*H > 65535, a pointer
  *   not aligned to its elements, a stride < 0 or > 2^40 / extent, a spec out of the
  *   ranges above (theta and scale finite, theta > 0, n_text <= L, every

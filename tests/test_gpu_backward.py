@@ -334,6 +334,48 @@ def test_layer_on_another_stream_and_positions(losa):
     assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
+def test_layer_with_positions_alone(losa):
+    """Listed positions stand for the grid: the rope's own may be another."""
+    B, H, d, block, L = 2, 2, 64, 32, 90
+    mask = make_mask(B * H, 3, 0.7, torch.Generator().manual_seed(2))
+    pat = pattern_of(losa, mask, B, H, block)
+    x = torch.randn(B, L, 3, H, d, device="cuda").to(BF)
+    dout = torch.randn(B, L, H, d, device="cuda").to(BF)
+    pos = torch.randint(0, 50, (B, L, 3), device="cuda", dtype=torch.int32)
+    both = []
+    for grid in ((2, 5, 9), (4, 4, 4)):
+        out, state = losa.layer_attn(*x.unbind(2), losa.Rope(grid, (16, 24, 24)), pat,
+                                     positions=pos)
+        both.append((out, *losa.layer_attn_bwd(dout, state)))
+    assert all(torch.equal(a, b) for a, b in zip(*both))
+
+
+def test_offsets_past_32_bits(losa):
+    """A layer of more than 2^31 elements a tensor: its first and last heads
+    give the bits that they give alone."""
+    B, H, d, block, n = 3, 22, 128, 128, 2047
+    L = n * block - 26
+    assert B * H * L * d > 2 ** 31
+    mask = torch.zeros(B * H, n, n, dtype=torch.bool)
+    i = torch.arange(n)
+    mask[:, i, i] = mask[:, i, n - 1 - i] = True
+    pat, one = pattern_of(losa, mask, B, H, block), pattern_of(losa, mask[:1], 1, 1, block)
+    rope = losa.Rope((L,), (d,))
+    x = torch.empty(B, L, 3, H, d, device="cuda", dtype=BF).normal_()
+    dout = torch.empty(B, L, H, d, device="cuda", dtype=BF).normal_()
+    dx = torch.empty_like(x)
+    out, state = losa.layer_attn(*x.unbind(2), rope, pat)
+    losa.layer_attn_bwd(dout, state, out=dx.unbind(2))
+    del state
+    for b, h in ((0, 0), (B - 1, H - 1)):
+        y, state = losa.layer_attn(*(t[b:b + 1, :, h:h + 1] for t in x.unbind(2)), rope, one)
+        assert torch.equal(out[b:b + 1, :, h:h + 1], y)
+        got = losa.layer_attn_bwd(dout[b:b + 1, :, h:h + 1], state)
+        for t, g in enumerate(got):
+            assert torch.equal(dx[b:b + 1, :, t, h:h + 1], g)
+    losa.check_status()
+
+
 def test_a_wait_that_runs_out(losa):
     """With a wait limit of one cycle the call gives up, the status says so,
     and the next call is whole again."""
@@ -450,6 +492,12 @@ def test_refusals(losa):
         a.update(change)
         with pytest.raises(losa.LosaError):
             losa.sparse_attn_bwd(**a)
+    need = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    bits = [torch.empty_like(q) for _ in range(3)]
+    ptr = [t.data_ptr() for t in (q, k, v, o, lse, do, *bits, need)]
+    assert losa.lib().losa_sparse_attn_bwd(  # lse halfway into an element
+        *ptr[:3], 0, ptr[3], 0, ptr[4] + 2, ptr[5], 0, d, L, 0.1, pat.handle, *ptr[6:9], 0, ptr[9],
+        1 << 20, None) == -1
     fresh = losa.import_pattern(*(pat.export("cpu")[x] for x in ("row_ptr", "col_idx")), B, H, 7,
                                 block, device="cuda")
     stream = torch.cuda.Stream()

@@ -8,6 +8,7 @@ import torch
 import block_sparse_attention_losa_b200 as losa
 
 FAKE = ctypes.c_void_p(0x10000)  # never dereferenced: the checks fail first
+OUT = [ctypes.c_void_p(0x100000 * i) for i in (1, 2, 3)]
 
 
 def _spec(n_axes=3, grid=(3, 5, 7), dim=(16, 24, 24), start=(0, 0, 0), scale=(1.0, 1.0, 1.0),
@@ -23,7 +24,7 @@ def _strides(B, L, H, d):
 
 def _rope(unpack, spec={}, **kw):
     a = dict(q=FAKE, k=FAKE, v=FAKE, in_dt=0, B=2, H=3, L=107, L_pad=128, d=64, pos=None,
-             qo=FAKE, ko=FAKE, vo=FAKE, out_dt=0)
+             qo=OUT[0], ko=OUT[1], vo=OUT[2], out_dt=0)
     a.update(kw)
     st = a.get("strides", _strides(2, 107, 3, 64))
     st = None if st is None else (ctypes.c_int64 * 9)(*st)
@@ -51,7 +52,8 @@ BAD = [
     dict(spec=dict(theta=0.0)), dict(spec=dict(theta=float("inf"))),
     dict(spec=dict(theta=float("nan"))), dict(spec=dict(scale=(1.0, float("nan"), 1.0))),
     dict(spec=dict(n_text=-1)), dict(spec=dict(n_text=108)), dict(spec=dict(pairing=2)),
-    dict(pos=FAKE, spec=dict(n_text=108)),
+    dict(pos=FAKE, spec=dict(n_text=108)), dict(pos=ctypes.c_void_p(0x10002)),
+    dict(qo=FAKE), dict(vo=FAKE), dict(qo=OUT[2]), dict(ko=OUT[0]), dict(vo=OUT[1]),
     dict(spec=dict(theta=1e-320, scale=(1.0, 1e10, 1.0))), dict(spec=dict(scale=(1e305, 1.0, 1.0))),
 ]
 
