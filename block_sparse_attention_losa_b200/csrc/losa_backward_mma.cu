@@ -165,6 +165,19 @@ __device__ __forceinline__ void tmem_st_bf16(uint32_t taddr, const float (&x)[32
   tmem_st16(taddr, pk);
 }
 
+// What that rounding leaves, rounded likewise: with it the pairs hold 16 bits
+// of each value.
+__device__ __forceinline__ void tmem_st_bf16_rest(uint32_t taddr, const float (&x)[32]) {
+  uint32_t pk[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t h = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    pk[i] = pack_bf16x2(x[2 * i] - __uint_as_float(h << 16),
+                        x[2 * i + 1] - __uint_as_float(h & 0xffff0000u));
+  }
+  tmem_st16(taddr, pk);
+}
+
 // Writes one row's 32 accumulator columns, times f, to the result.
 template <bool kOutBf16>
 __device__ __forceinline__ void store_row32(void* out, size_t at, const float (&x)[32], float f) {
@@ -592,7 +605,9 @@ template <int D> struct QueryLayout {
 // products read from shared memory. Per step j the MMA thread issues S(j+1)
 // as soon as the softmax has S(j) in registers, then dQ(j) and dP(j+1); dS
 // takes dP's place as the A operand of dQ += dS K.
-template <int D, int BLK, bool kOutBf16>
+// kRest: dS is followed by what its rounding to bf16 left, and dQ is the sum
+// of both products (see launch_backward_mma).
+template <int D, int BLK, bool kOutBf16, bool kRest>
 __device__ __forceinline__ void query_tile(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                            const BwdParams& p, const BwdLists& list, int tile) {
   using Lay = QueryLayout<D>;
@@ -744,6 +759,12 @@ __device__ __forceinline__ void query_tile(const CUtensorMap& tm_k, const CUtens
         for (int i = 0; i < 4; ++i)
           mma_ts(tmem + C_DQ, at + (i >> 1) * 64 + (i & 1) * 8,
                  b + (((i >> 1) * 64 + (i & 1) * 16) * 128 >> 4), IDESC_G, i > 0 ? 1u : acc);
+        if constexpr (kRest) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mma_ts(tmem + C_DQ, at + 32 + (i >> 1) * 64 + (i & 1) * 8,
+                   b + (((i >> 1) * 64 + (i & 1) * 16) * 128 >> 4), IDESC_G, 1u);
+        }
         if (done) umma_commit(done);
       }
       __syncwarp();
@@ -866,10 +887,12 @@ __device__ __forceinline__ void query_tile(const CUtensorMap& tm_k, const CUtens
       gradient(y0, w0, lim[0]);
       tmem_st_bf16(dp_col, y0);
       tmem_ld_wait();
+      if constexpr (kRest) tmem_st_bf16_rest(dp_col + 32, y0);  // where y1 was
       tmem_st_wait();
       warp_arrive(&ds_full[0], lane);
       gradient(y1, w1, lim[1]);
       tmem_st_bf16(dp_col + 16, y1);
+      if constexpr (kRest) tmem_st_bf16_rest(dp_col + 48, y1);
       tmem_st_wait();
       warp_arrive(&ds_full[1], lane);
       if (j + 1 < n_it) ok = weights(j + 1);
@@ -904,7 +927,7 @@ __device__ __forceinline__ void query_tile(const CUtensorMap& tm_k, const CUtens
 // have four products, then the query tiles, whose steps have three. The
 // query tiles fill the SMs that the last key tiles leave idle, and a small
 // call's two halves run side by side.
-template <int D, int BLK, bool kOutBf16>
+template <int D, int BLK, bool kOutBf16, bool kRest>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     bwd_tiles_kernel(const __grid_constant__ CUtensorMap own_k,
                      const __grid_constant__ CUtensorMap own_v,
@@ -916,10 +939,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   if (i < p.n_tiles)
     key_tile<D, BLK, kOutBf16>(own_k, own_v, step_q, step_do, p, p.keys, p.keys.order[i]);
   else
-    query_tile<D, BLK, kOutBf16>(step_k, step_v, p, p.queries, p.queries.order[i - p.n_tiles]);
+    query_tile<D, BLK, kOutBf16, kRest>(step_k, step_v, p, p.queries, p.queries.order[i - p.n_tiles]);
 }
 
-template <int D, int BLK, bool kOutBf16>
+template <int D, int BLK, bool kOutBf16, bool kRest>
 cudaError_t run_mma(const BackwardCall& c, const BackwardOperands& w, const BwdParams& p,
                     cudaStream_t stream) {
   const int BH = c.p->B * c.p->H;
@@ -932,7 +955,7 @@ cudaError_t run_mma(const BackwardCall& c, const BackwardOperands& w, const BwdP
       !make_slab_map(&step_k, c.k, BH, c.L, p.L_pad, D, BLK, 2, false) ||
       !make_slab_map(&step_v, c.v, BH, c.L, p.L_pad, D, BLK, 2, false))
     return cudaErrorInvalidValue;
-  auto kern = bwd_tiles_kernel<D, BLK, kOutBf16>;
+  auto kern = bwd_tiles_kernel<D, BLK, kOutBf16, kRest>;
   constexpr int smem = std::max(KeyLayout<D>::SMEM_ALLOC, QueryLayout<D>::SMEM_ALLOC);
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t err = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed);
@@ -968,10 +991,22 @@ cudaError_t launch_backward_mma(const BackwardCall& c, const BackwardOperands& w
   p.status = device_status_word();
   if (!p.status) return cudaErrorInvalidDevice;
   p.wait_limit = wait_limit();
-#define LOSA_BWD_CASE(D_, BLK_)                                       \
-  if (c.d == D_ && pat->block == BLK_)                                \
-    return c.out_bf16 ? run_mma<D_, BLK_, true>(c, w, p, stream)      \
-                      : run_mma<D_, BLK_, false>(c, w, p, stream);
+  // dQ is a sum that cancels (each row of dS sums to 0), and dS's rounding to
+  // bf16 shows in it: by 0.3 % of its norm. In calls of few rows, over which
+  // that does not average out, it was 0.5 to 1 % in one of 300. There the query
+  // tiles, which have one product less than the key tiles beside them, take
+  // dS's remainder as well: 0.17 %, the result's own rounding, for 3 to 5 % of
+  // the time (one head of 2,000 tokens, half the blocks kept: d 128 26.8 ->
+  // 28.1 us, d 64 24.1 -> 24.9). It would cost 7 and 13 % at one head of 9,000
+  // tokens and 11 to 14 % where the tiles fill the GPU.
+  const bool rest = p.n_tiles <= 32;
+#define LOSA_BWD_CASE(D_, BLK_)                                                    \
+  if (c.d == D_ && pat->block == BLK_) {                                           \
+    auto run = c.out_bf16                                                          \
+                   ? (rest ? run_mma<D_, BLK_, true, true> : run_mma<D_, BLK_, true, false>)    \
+                   : (rest ? run_mma<D_, BLK_, false, true> : run_mma<D_, BLK_, false, false>); \
+    return run(c, w, p, stream);                                                   \
+  }
   LOSA_BWD_CASE(128, 128)
   LOSA_BWD_CASE(128, 64)
   LOSA_BWD_CASE(128, 32)

@@ -300,8 +300,9 @@ int losa_pattern_export_bwd(const losa_pattern* p, int64_t* entries, int32_t* ke
  *   take weight 0, and 0 times infinity or NaN is NaN. No output may overlap
  *   an input, the workspace or another output (equal addresses are refused).
  *   bf16 q, k, v run on tensor cores: P and dS are rounded to bf16 as their
- *   operands (half a unit in the 8th bit each), as is a fp32 d_o; all sums
- *   are fp32. fp32 q, k, v run in fp32 throughout (no tf32 rounding). No
+ *   operands (half a unit in the 8th bit each), as is a fp32 d_o; dQ takes
+ *   dS with 16 bits in calls of at most 32 tiles of 128 rows, over which its
+ *   rounding errors would not average out; all sums are fp32. fp32 q, k, v run in fp32 throughout (no tf32 rounding). No
  *   atomics: a call's results are the same bits every time.
  *   Does not allocate or synchronise, so it can be captured in a CUDA graph.
  *   Returns LOSA_ERR_ARG for a null or misaligned pointer (16 bytes; lse 4),

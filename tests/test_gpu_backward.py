@@ -163,6 +163,53 @@ def test_flat_and_peaked_rows(losa, dtype, spread):
     losa.check_status()
 
 
+@pytest.mark.parametrize("block,d,L", [(32, 64, 33), (64, 128, 64), (128, 64, 97), (32, 128, 90)])
+def test_dq_of_small_calls(losa, block, d, L):
+    """In calls of few rows dQ takes dS with 16 bits, so that what the keys
+    have in common cancels: here all share a long part and some a longer
+    one."""
+    B, H, n = 1, 2, -(-L // block)
+    g = torch.Generator().manual_seed(d + L)
+    mask = make_mask(B * H, n, 0.8, g)
+    pat = pattern_of(losa, mask, B, H, block)
+    x = torch.randn(4, B * H, L, d, generator=g).to("cuda")
+    x[0] *= 0.1
+    x[1] += 3 * torch.randn(B * H, 1, d, generator=g).to("cuda")
+    x[1, :, ::9] += 10 * torch.randn(B * H, 1, d, generator=g).to("cuda")
+    q, k, v, do = x.to(BF).double()
+    keep, scale, t = token_mask(mask, block, L).cuda(), 1 / math.sqrt(d), lambda y: y.transpose(1, 2)
+    o, lse = forward64(q, k, v, keep, scale)
+    o, lse = o.float().double(), lse.float().double()
+    z = (q @ t(k)) * scale - lse[..., None]
+    p = torch.where(keep, torch.exp(z), 0.0)
+    dd = (do @ t(v)) - (do * o).sum(-1, keepdim=True)
+    ds = p * dd
+    # A term of a tensor-core sum is off by at most a step (2 U) of the sum of
+    # magnitudes, one of D's fp32 sum by U; the exponential by 3.1e-7 < 6 U and
+    # its argument's roundings; dS by V of what its rounding left, V of it; dQ
+    # sums 2 L terms.
+    es = 2 * (d + 4) * U * scale * (q.abs() @ t(k.abs())) + 4 * U * (z.abs() + lse.abs()[..., None])
+    ed = (d + 4) * U * (2 * do.abs() @ t(v.abs()) + (do * o).abs().sum(-1, keepdim=True))
+    e = p * (torch.expm1(es) + 8 * U) * dd.abs() + p * ed
+    e = e + V * V * (ds.abs() + e)
+    tol = scale * (e @ k.abs() + 4 * (L + 8) * U * (ds.abs() @ k.abs()))
+
+    def padded(y, dt):
+        z = torch.zeros((B * H, n * block) + y.shape[2:], device="cuda", dtype=dt)
+        z[:, :L] = y.to(dt)
+        return z.view(B, H, n * block, *y.shape[2:])
+
+    dq = losa.sparse_attn_bwd(padded(q, BF), padded(k, BF), padded(v, BF), padded(o, F32),
+                              padded(lse, F32), padded(do, BF), L, pat, out_dtype=F32)[0]
+    want = scale * (ds @ k)
+    got = dq.flatten(0, 1)[:, :L].double()
+    assert ((got - want).abs() - tol * (1 + U) - U * want.abs()).max().item() <= 0
+    # dS rounded once would be off by more than that.
+    once = scale * (ds.to(BF).double() @ k)
+    assert ((once - want).abs() - tol).max().item() > 0
+    losa.check_status()
+
+
 @pytest.mark.parametrize("block,d", [(32, 64), (64, 128), (128, 128), (32, 128), (128, 64)])
 def test_lists_by_key_are_the_transposed_pattern(losa, block, d):
     B, H, n = 2, 2, 21
