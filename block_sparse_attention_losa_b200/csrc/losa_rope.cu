@@ -14,8 +14,8 @@
 // and pair and stay in registers for every head of both tensors. Pairs by
 // halves meet in different threads of a warp: they exchange through shared
 // memory.
-// Measured on a B200 with cold caches, bf16, launch included: 105 us at the
-// Wan2.1-1.3B shape (12 heads, 32,760 tokens, d 128: 5.7 TB/s), 684 us at
+// Measured on a B200 with cold caches, bf16, launch included: 102 us at the
+// Wan2.1-1.3B shape (12 heads, 32,760 tokens, d 128: 5.9 TB/s), 686 us at
 // the HunyuanVideo one (24 heads, 118,800 tokens: 6.4 TB/s, 0.99 of the
 // measured copy rate); by halves 110 us at the first. Tried and slower: 16
 // features a thread in two groups of 128 contiguous bytes a row (862 us at
