@@ -340,20 +340,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
         }
       }
-      if (!ok) {
-        // Aborted: wait (bounded) for the copies still in flight before the
-        // CTA releases its shared memory.
-        mbar_wait_drain(&q_full[0], 0);
-        mbar_wait_drain(&q_full[1], 0);
-        for (int i = (kc > NSK ? kc - NSK : 0); i < kc; ++i) mbar_wait_drain(&k_full[i % NSK], (i / NSK) & 1);
-        for (int i = (vc > NSV ? vc - NSV : 0); i < vc; ++i) mbar_wait_drain(&v_full[i % NSV], (i / NSV) & 1);
-      } else {
-        // A tile slot with no work (the last CTA of an odd tile count):
-        // nobody else waits for its Q copy, so let it land before exit.
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (n_it[t] == 0) mbar_wait_drain(&q_full[t], 0);
-      }
+      // The last copies land (bounded wait) before the CTA releases its shared
+      // memory, also when another warp gave up a wait after all of them had
+      // been sent, and those of a tile slot with no work (the last CTA of an
+      // odd tile count), whose Q nobody else waits for.
+      mbar_wait_drain(&q_full[0], 0);
+      mbar_wait_drain(&q_full[1], 0);
+      for (int i = (kc > NSK ? kc - NSK : 0); i < kc; ++i) mbar_wait_drain(&k_full[i % NSK], (i / NSK) & 1);
+      for (int i = (vc > NSV ? vc - NSV : 0); i < vc; ++i) mbar_wait_drain(&v_full[i % NSV], (i / NSV) & 1);
     }
   } else if (warp == 9) {
     // ================================================================ MMA issuer
@@ -522,11 +516,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
         }
       }
-      if (!ok) {
-        // Drain: let every MMA issued so far finish before TMEM is freed.
-        umma_commit(drain_bar);
-        mbar_wait_drain(drain_bar, 0);
-      }
+      // Every MMA issued finishes before TMEM is freed, also when a softmax
+      // warp gave up waiting for the last ones.
+      umma_commit(drain_bar);
+      mbar_wait_drain(drain_bar, 0);
     }
   }
   } else {

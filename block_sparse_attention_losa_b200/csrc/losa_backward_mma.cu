@@ -387,15 +387,14 @@ __device__ __forceinline__ void key_tile(const CUtensorMap& tm_k, const CUtensor
         load_step(&tm_do, p.do_aug, &do_full[st], Lay::OFF_DO, Lay::OFF_DA, st, row);
         ++loaded_do;
       }
-      if (!ok) {
-        // Aborted: let the copies in flight land before the CTA ends.
-        mbar_wait_drain(k_full, 0);
-        mbar_wait_drain(v_full, 0);
-        for (int i = max(loaded_q - NS, 0); i < loaded_q; ++i)
-          mbar_wait_drain(&q_full[i % NS], (i / NS) & 1);
-        for (int i = max(loaded_do - NS, 0); i < loaded_do; ++i)
-          mbar_wait_drain(&do_full[i % NS], (i / NS) & 1);
-      }
+      // The last copies land before the CTA ends, also when another warp gave
+      // up a wait after all of them had been sent.
+      mbar_wait_drain(k_full, 0);
+      mbar_wait_drain(v_full, 0);
+      for (int i = max(loaded_q - NS, 0); i < loaded_q; ++i)
+        mbar_wait_drain(&q_full[i % NS], (i / NS) & 1);
+      for (int i = max(loaded_do - NS, 0); i < loaded_do; ++i)
+        mbar_wait_drain(&do_full[i % NS], (i / NS) & 1);
     }
   } else if (warp == 9) {
     // ================================================================ MMA issuer
@@ -478,9 +477,11 @@ __device__ __forceinline__ void key_tile(const CUtensorMap& tm_k, const CUtensor
           issue_scores(C_DP, Lay::OFF_V, Lay::OFF_DO, Lay::OFF_DA, nx, dp_full);
         }
       }
-      // The end of the MMAs: for the results, or (aborted) before TMEM is freed.
-      if (elect_one()) umma_commit(ok ? acc_full : drain_bar);
-      if (!ok) mbar_wait_drain(drain_bar, 0);
+      // The end of the MMAs: for the results, and before TMEM is freed, also
+      // when the warps that want the results gave up waiting for them.
+      uint64_t* end = ok ? acc_full : drain_bar;
+      if (elect_one()) umma_commit(end);
+      mbar_wait_drain(end, 0);
     }
   }
   } else {
@@ -723,12 +724,11 @@ __device__ __forceinline__ void query_tile(const CUtensorMap& tm_k, const CUtens
         load_step(&tm_v, &v_full[st], Lay::OFF_V, st, row);
         ++loaded_v;
       }
-      if (!ok) {
-        for (int i = max(loaded_k - NS, 0); i < loaded_k; ++i)
-          mbar_wait_drain(&k_full[i % NS], (i / NS) & 1);
-        for (int i = max(loaded_v - NS, 0); i < loaded_v; ++i)
-          mbar_wait_drain(&v_full[i % NS], (i / NS) & 1);
-      }
+      // The last copies land before the CTA ends, as in key_tile.
+      for (int i = max(loaded_k - NS, 0); i < loaded_k; ++i)
+        mbar_wait_drain(&k_full[i % NS], (i / NS) & 1);
+      for (int i = max(loaded_v - NS, 0); i < loaded_v; ++i)
+        mbar_wait_drain(&v_full[i % NS], (i / NS) & 1);
     }
   } else if (warp == 9) {
     // ================================================================ MMA issuer
@@ -799,8 +799,9 @@ __device__ __forceinline__ void query_tile(const CUtensorMap& tm_k, const CUtens
         issue_scores(C_DP, C_DO, Lay::OFF_V, nx, dp_full, &v_empty[nx]);
       }
     }
-    if (elect_one()) umma_commit(ok ? acc_full : drain_bar);
-    if (!ok) mbar_wait_drain(drain_bar, 0);
+    uint64_t* end = ok ? acc_full : drain_bar;
+    if (elect_one()) umma_commit(end);
+    mbar_wait_drain(end, 0);
   }
   } else {
     reg_alloc<kScoreRegs>();

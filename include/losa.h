@@ -449,8 +449,9 @@ int losa_check_status(void* stream);
  * sets, for the whole process, how many SM cycles a wait inside the
  * attention kernels spins before it gives up (1 <= limit_cycles <= 2^33),
  * or restores the default (about 2 s at the B200's clock) when limit_cycles
- * is 0. It applies to the losa_dense_mass and losa_sparse_attn launches made
- * after the call. A kernel whose wait runs out records LOSA_ERR_TIMEOUT in
+ * is 0. It applies to the losa_dense_mass, losa_dense_mass_select,
+ * losa_sparse_attn and losa_sparse_attn_bwd (bf16) launches made after the
+ * call. A kernel whose wait runs out records LOSA_ERR_TIMEOUT in
  * the device status word, and every warp of the CTA then leaves its loop,
  * lets the copies and MMAs it issued finish, frees its tensor memory and
  * returns, so the CUDA context stays usable. With a limit of a few cycles a
