@@ -385,17 +385,21 @@ def sparse_attn_bwd(q, k, v, o, lse, do, L, pattern: Pattern, scale=None, out_dt
     pattern.prepare_backward() has been called on: o and lse are what the
     forward call returned for q, k, v, do is the gradient of o. The results
     have q's dtype unless out_dtype or the outputs say otherwise. Rows >= L of
-    the inputs are not used; those of the results are 0."""
+    the inputs are not used; those of the results are 0. For fp32 q, k, v both
+    o and lse may be None: what is needed of them is then formed in fp32,
+    without the forward call's tf32 roundings (see losa.h)."""
     _check_qkv(q, k, v)
     shape, device = q.shape, q.device
     B, H, Lp, d = shape
     if (B, H, Lp) != (pattern.B, pattern.H, pattern.n_blocks * pattern.block):
         raise ValueError("q/k/v shape does not match the pattern")
+    if (o is None) != (lse is None) or (o is None and q.dtype != torch.float32):
+        raise ValueError("o and lse must be given, or, for fp32 q, k, v, both left out")
     for name, t in (("o", o), ("do", do)):
-        if not (t.shape == shape and t.device == device and t.is_contiguous()):
+        if t is not None and not (t.shape == shape and t.device == device and t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous tensor of q's shape and device")
-    if not (lse.shape == shape[:3] and lse.dtype == torch.float32 and lse.device == device
-            and lse.is_contiguous()):
+    if lse is not None and not (lse.shape == shape[:3] and lse.dtype == torch.float32
+                                and lse.device == device and lse.is_contiguous()):
         raise ValueError("lse must be a contiguous fp32 tensor [B, H, L_pad] on q's device")
     if not device == k.device == v.device == pattern.device:
         raise ValueError("q, k, v and the pattern must be on one device")
@@ -421,8 +425,8 @@ def sparse_attn_bwd(q, k, v, o, lse, do, L, pattern: Pattern, scale=None, out_dt
         elif not (workspace.device == device and workspace.is_contiguous()):
             raise ValueError("workspace must be a contiguous tensor on q's device")
         st = _lib.losa_sparse_attn_bwd(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), in_code, o.data_ptr(), _dtype_code(o),
-            lse.data_ptr(), do.data_ptr(), do_code, d, int(L), float(scale), pattern.handle,
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), in_code, _ptr(o),
+            LOSA_FP32 if o is None else _dtype_code(o), _ptr(lse), do.data_ptr(), do_code, d, int(L), float(scale), pattern.handle,
             dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _dtype_code(dq), workspace.data_ptr(),
             workspace.nbytes, _raw_stream(stream, device))
     _check("losa_sparse_attn_bwd", st)
@@ -630,7 +634,9 @@ def layer_attn_bwd(dout, state: LayerState, out=None, stream=None):
     with _on(stream, dout.device):
         do = rope_pack(None, None, dout, s.pattern.block, s.rope, positions=s.positions,
                        stream=stream)[2]
-        grads = sparse_attn_bwd(s.q, s.k, s.v, s.o, s.lse, do, s.L, s.pattern, scale=s.scale,
+        # fp32: the forward call's O and lse carry its tf32 roundings.
+        o, lse = (None, None) if s.q.dtype == torch.float32 else (s.o, s.lse)
+        grads = sparse_attn_bwd(s.q, s.k, s.v, o, lse, do, s.L, s.pattern, scale=s.scale,
                                 stream=stream)
         return rope_unpack(*grads, s.L, s.rope, positions=s.positions, out=out, stream=stream)
 

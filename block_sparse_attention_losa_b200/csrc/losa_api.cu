@@ -440,8 +440,8 @@ int losa_sparse_attn_bwd(const void* q, const void* k, const void* v, int in_dty
                          int L, float scale, const losa_pattern* p, void* dq, void* dk, void* dv,
                          int out_dtype, void* workspace, int64_t workspace_bytes, void* stream) {
   NvtxRange nvtx_range("losa_sparse_attn_bwd");
-  if (!q || !k || !v || !o || !lse || !d_o || !p || !dq || !dk || !dv || !workspace)
-    return LOSA_ERR_ARG;
+  if (!q || !k || !v || !d_o || !p || !dq || !dk || !dv || !workspace) return LOSA_ERR_ARG;
+  if (!o != !lse || (!o && in_dtype != LOSA_FP32)) return LOSA_ERR_ARG;
   if (!valid_dtype(in_dtype) || !valid_dtype(o_dtype) || !valid_dtype(do_dtype) ||
       !valid_dtype(out_dtype))
     return LOSA_ERR_ARG;

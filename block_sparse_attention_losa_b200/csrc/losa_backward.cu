@@ -19,6 +19,11 @@
 //
 // This file holds the prepass (D, and what the tensor-core path reads beside
 // it) and the fp32 path; losa_backward_mma.cu the bf16 path.
+//
+// fp32 calls without o and lse form lse_i and D_i themselves, from the scores
+// that P is made of. The forward call's own come from tf32 products: with them
+// a row of P does not sum to 1 and sum_j dS_ij is not 0, so what a head's keys
+// have in common stands in dQ, magnified by its size over the keys' spread.
 #include <algorithm>
 
 #include "losa_device.cuh"
@@ -73,6 +78,7 @@ struct AugRows {
 // dO's type is not that of q, k and v, `copy` receives it in theirs: a fp32 dO
 // is rounded to bf16, as the tensor cores read it, before D is formed, so that
 // D cancels against the same dO that dP is made of; a bf16 one is widened.
+// Without o (fp32 path, D formed later) dO is converted only.
 // Bound: HBM. D / 8 lanes share a row, and a warp has four sets of rows in
 // flight (one row per warp at a time took 20 us at 75,776 rows of 64).
 constexpr int kDeltaSets = 4;
@@ -91,7 +97,7 @@ __global__ void __launch_bounds__(256)
     const int64_t row = row0 + s * SET;
     valid[s] = row < rows && row % L_pad < L;
     if (valid[s]) {
-      a[s].load(o, o_bf16, size_t(row) * D + part * 8);
+      if (o) a[s].load(o, o_bf16, size_t(row) * D + part * 8);
       b[s].load(d_o, do_bf16, size_t(row) * D + part * 8);
     }
   }
@@ -100,8 +106,8 @@ __global__ void __launch_bounds__(256)
     const int64_t row = row0 + s * SET;
     float sum = 0.f;
     if (valid[s]) {
-      float x[8], y[8];
-      a[s].get(o_bf16, x);
+      float x[8] = {}, y[8];
+      if (o) a[s].get(o_bf16, x);
       b[s].get(do_bf16, y);
       if (copy) {
         const size_t at = size_t(row) * D + part * 8;
@@ -144,6 +150,7 @@ __global__ void __launch_bounds__(256)
 
 struct FmaParams {
   const float *q, *k, *v, *d_o, *lse, *delta;
+  float *lse_out, *delta_out;  // row_stats_kernel's results
   int L, L_pad, n_qt, n_tiles, block;
   float scale;
   const int *key_ptr, *key_entry, *key_order;        // by key tile
@@ -188,6 +195,24 @@ __device__ __forceinline__ void dot4(const float4& a, const float4& b, f32x2& ac
   acc = f2_fma(f2_make(a.z, a.w), f2_make(b.z, b.w), acc);
 }
 
+// Running maximum m of a row's scores, and of exp(s - m) the sum l and the sum
+// t of its products with dP. lse = m + log l, D = t / l.
+struct RowStats {
+  float m, l, t;
+};
+// exp(from - to), 0 for a sum that is still empty.
+__device__ __forceinline__ float raised(float from, float to) {
+  return from == to ? 1.f : from == -INFINITY ? 0.f : expf(from - to);
+}
+__device__ __forceinline__ RowStats join(const RowStats& a, const RowStats& b) {
+  const float m = fmaxf(a.m, b.m), fa = raised(a.m, m), fb = raised(b.m, m);
+  return {m, a.l * fa + b.l * fb, a.t * fa + b.t * fb};
+}
+
+// What fma_tile forms: dK and dV of key rows, dQ of query rows, or their lse
+// and D.
+enum class Fma { kKeys, kQueries, kStats };
+
 // One CTA owns 32 rows (a quarter of a 128-row tile, always inside one block)
 // of keys (kKeys: dK and dV) or of queries (dQ) and walks those list entries
 // whose blocks meet, 64 rows of the other side at a time: two segments of 32
@@ -205,9 +230,10 @@ __device__ __forceinline__ void dot4(const float4& a, const float4& b, f32x2& ac
 //   at the end.
 // 5,000 tokens, 8 heads, d 64, half the blocks kept: 2.38 ms, 27 TFLOP/s of
 // the five products that the gradient needs, 38 of the seven that run.
-template <int D, int T, bool kKeys>
+template <int D, int T, Fma kWhat>
 __device__ __forceinline__ void fma_tile(const FmaParams& p, FmaSmem<D>& sm, int tile,
                                          int quarter) {
+  constexpr bool kKeys = kWhat == Fma::kKeys, kStats = kWhat == Fma::kStats;
   constexpr int CH = D / 4;                           // chunks of a row
   constexpr int PER = CH / 2 * (kOwn / 8);            // threads that hold a gradient
   constexpr int GROUPS = T / PER;
@@ -275,8 +301,11 @@ __device__ __forceinline__ void fma_tile(const FmaParams& p, FmaSmem<D>& sm, int
   const bool use_p = kKeys && (group & 1);
   const int gpart = kKeys ? group >> 1 : group;
   f32x2 acc[4][8] = {};  // pairs of own rows x features
+  RowStats stats[4];
+#pragma unroll
+  for (int a = 0; a < 4; ++a) stats[a] = {-INFINITY, 0.f, 0.f};
   float own_lse[4], own_delta[4];
-  if (!kKeys) {
+  if (kWhat == Fma::kQueries) {
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
       const int r = own0 + so + 4 * a;
@@ -330,6 +359,27 @@ __device__ __forceinline__ void fma_tile(const FmaParams& p, FmaSmem<D>& sm, int
 #pragma unroll
         for (int i = 0; i < NI; ++i) dot4(xv[a], yv[i], d2[a][i]);
     }
+    if constexpr (kStats) {
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        RowStats& z = stats[a];
+        float m = z.m;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+          if (on[i]) m = fmaxf(m, f2_sum(s2[a][i]) * p.scale);
+        const float f = raised(z.m, m);
+        z = {m, z.l * f, z.t * f};
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          if (!on[i]) continue;
+          const float w = expf(fmaf(f2_sum(s2[a][i]), p.scale, -m));
+          z.l += w;
+          z.t = fmaf(w, f2_sum(d2[a][i]), z.t);
+        }
+      }
+      __syncthreads();  // before the next step's rows arrive
+      continue;
+    }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int r = si + 8 * i;
@@ -371,9 +421,36 @@ __device__ __forceinline__ void fma_tile(const FmaParams& p, FmaSmem<D>& sm, int
     __syncthreads();  // before the next step's rows arrive
   }
 
-  // Parts of a gradient meet in shared memory; the first one writes the rows.
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
+  if constexpr (kStats) {
+    // A row's sums lie in eight lanes of the T / 64 warps that share it.
+    constexpr int SHARES = T / 64;
+    static_assert(SHARES * kOwn * sizeof(RowStats) <= sizeof(sm.p), "room for the rows' sums");
+    RowStats* sums = reinterpret_cast<RowStats*>(&sm.p[0][0]);
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+#pragma unroll
+      for (int bit : {2, 8, 16}) {
+        const RowStats& z = stats[a];
+        stats[a] = join(z, {__shfl_xor_sync(0xffffffffu, z.m, bit),
+                            __shfl_xor_sync(0xffffffffu, z.l, bit),
+                            __shfl_xor_sync(0xffffffffu, z.t, bit)});
+      }
+      if ((lane & ~5) == 0) sums[(warp % SHARES) * kOwn + so + 4 * a] = stats[a];
+    }
+    __syncthreads();
+    if (tid < kOwn && own0 + tid < p.L) {
+      RowStats z = sums[tid];
+#pragma unroll
+      for (int s = 1; s < SHARES; ++s) z = join(z, sums[s * kOwn + tid]);
+      p.lse_out[base + own0 + tid] = z.m + logf(z.l);
+      p.delta_out[base + own0 + tid] = z.t / z.l;
+    }
+    return;
+  }
+
+  // Parts of a gradient meet in shared memory; the first one writes the rows.
   float out[8][8];
 #pragma unroll
   for (int a = 0; a < 4; ++a)
@@ -430,14 +507,32 @@ __global__ void __launch_bounds__(T, T == 128 ? 2 : 1) bwd_fma_kernel(const FmaP
   FmaSmem<D>& sm = *reinterpret_cast<FmaSmem<D>*>(smem_raw);
   const int i = blockIdx.x >> 2, quarter = blockIdx.x & 3;
   if (i < p.n_tiles)
-    fma_tile<D, T, true>(p, sm, p.key_order[i], quarter);
+    fma_tile<D, T, Fma::kKeys>(p, sm, p.key_order[i], quarter);
   else
-    fma_tile<D, T, false>(p, sm, p.tile_order[i - p.n_tiles], quarter);
+    fma_tile<D, T, Fma::kQueries>(p, sm, p.tile_order[i - p.n_tiles], quarter);
+}
+
+// lse and D of the query quarters, in a launch of its own since the key tiles
+// need every row's: two products more for the gradient's seven (2,200 tokens, 4
+// heads, d 128, half the blocks kept: 531 -> 729 us).
+template <int D, int T>
+__global__ void __launch_bounds__(T, T == 128 ? 2 : 1) row_stats_kernel(const FmaParams p) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  fma_tile<D, T, Fma::kStats>(p, *reinterpret_cast<FmaSmem<D>*>(smem_raw),
+                              p.tile_order[blockIdx.x >> 2], blockIdx.x & 3);
 }
 
 template <int D, int T> cudaError_t run_fma(const FmaParams& p, cudaStream_t stream) {
-  static std::atomic<uint64_t> allowed{0};
-  const cudaError_t err = allow_smem(reinterpret_cast<const void*>(bwd_fma_kernel<D, T>),
+  static std::atomic<uint64_t> allowed{0}, stats_allowed{0};
+  cudaError_t err;
+  if (p.lse_out) {
+    err = allow_smem(reinterpret_cast<const void*>(row_stats_kernel<D, T>),
+                     int(sizeof(FmaSmem<D>)), stats_allowed);
+    if (err != cudaSuccess) return err;
+    row_stats_kernel<D, T><<<4u * unsigned(p.n_tiles), T, sizeof(FmaSmem<D>), stream>>>(p);
+    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+  }
+  err = allow_smem(reinterpret_cast<const void*>(bwd_fma_kernel<D, T>),
                                      int(sizeof(FmaSmem<D>)), allowed);
   if (err != cudaSuccess) return err;
   bwd_fma_kernel<D, T><<<8u * unsigned(p.n_tiles), T, sizeof(FmaSmem<D>), stream>>>(p);
@@ -448,16 +543,17 @@ template <int D, int T> cudaError_t run_fma(const FmaParams& p, cudaStream_t str
 
 namespace {
 // Offsets of a call's workspace: D, the bf16 path's further operand rows, and
-// dO in the type of q, k and v where it has the other one. Rows come in
-// multiples of 32, so each part is aligned to 128 bytes.
+// dO in the type of q, k and v where it has the other one, and the fp32 path's
+// own lse. Rows come in multiples of 32, so each part is aligned to 128 bytes.
 struct Workspace {
-  size_t q_aug, do_aug, copy, bytes;
+  size_t q_aug, do_aug, copy, lse, bytes;
   Workspace(const losa_pattern* p, int d, bool in_bf16, bool do_bf16) {
     const size_t rows = size_t(p->B) * p->H * p->n_blocks * p->block;
     q_aug = rows * 4;
     do_aug = q_aug + (in_bf16 ? rows * 32 : 0);
     copy = do_aug + (in_bf16 ? rows * 32 : 0);
-    bytes = copy + (in_bf16 != do_bf16 ? rows * d * (in_bf16 ? 2 : 4) : 0);
+    lse = copy + (in_bf16 != do_bf16 ? rows * d * (in_bf16 ? 2 : 4) : 0);
+    bytes = lse + (in_bf16 ? 0 : rows * 4);
   }
 };
 }  // namespace
@@ -481,10 +577,12 @@ cudaError_t launch_backward(const BackwardCall& c, cudaStream_t stream) {
            1.f / c.scale};
   const int64_t per_cta = 8 * kDeltaSets * (256 / c.d);
   const unsigned grid = unsigned((rows + per_cta - 1) / per_cta);
-  (c.d == 64 ? delta_kernel<64> : delta_kernel<128>)<<<grid, 256, 0, stream>>>(
-      c.o, c.o_bf16, c.d_o, c.do_bf16, rows, c.L, L_pad, delta, copy, aug);
-  cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess) return err;
+  if (c.o || copy) {
+    (c.d == 64 ? delta_kernel<64> : delta_kernel<128>)<<<grid, 256, 0, stream>>>(
+        c.o, c.o_bf16, c.d_o, c.do_bf16, rows, c.L, L_pad, delta, copy, aug);
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+  }
   if (c.in_bf16)
     return launch_backward_mma(c, {d_o, delta,
                                    reinterpret_cast<const uint16_t*>(ws + at.q_aug),
@@ -495,7 +593,9 @@ cudaError_t launch_backward(const BackwardCall& c, cudaStream_t stream) {
   p.k = static_cast<const float*>(c.k);
   p.v = static_cast<const float*>(c.v);
   p.d_o = static_cast<const float*>(d_o);
-  p.lse = c.lse;
+  p.lse_out = c.o ? nullptr : reinterpret_cast<float*>(ws + at.lse);
+  p.delta_out = delta;
+  p.lse = c.o ? c.lse : p.lse_out;
   p.delta = delta;
   p.L = c.L;
   p.L_pad = L_pad;

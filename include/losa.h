@@ -285,7 +285,13 @@ int losa_pattern_export_bwd(const losa_pattern* p, int64_t* entries, int32_t* ke
  *
  *   q, k, v   [B, H, L_pad, d] device, in_dtype: the forward call's inputs.
  *   o, lse    what the forward call returned for them: O (o_dtype) and the
- *             row log-sum-exp over the retained keys.
+ *             row log-sum-exp over the retained keys. With fp32 q, k, v both
+ *             may be NULL: lse and D are then formed in fp32 from the call's
+ *             own scores, two more products for the seven that run. An fp32
+ *             losa_sparse_attn's O and lse carry its tf32 roundings, which do
+ *             not cancel against fp32 scores: with them dQ was off by 5e-4,
+ *             2e-3 and 2e-2 of its norm for keys whose common part is 1, 3
+ *             and 10 times their spread. Training in fp32 passes NULL.
  *   d_o       [B, H, L_pad, d], do_dtype: the gradient of O.
  *   dq, dk, dv  [B, H, L_pad, d], out_dtype, written whole; rows >= L are 0.
  *             With P_ij = exp(scale q_i.k_j - lse_i) on the kept pairs and
