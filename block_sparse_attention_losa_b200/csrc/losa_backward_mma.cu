@@ -993,14 +993,18 @@ cudaError_t launch_backward_mma(const BackwardCall& c, const BackwardOperands& w
   if (!p.status) return cudaErrorInvalidDevice;
   p.wait_limit = wait_limit();
   // dQ is a sum that cancels (each row of dS sums to 0), and dS's rounding to
-  // bf16 shows in it: by 0.3 % of its norm. In calls of few rows, over which
-  // that does not average out, it was 0.5 to 1 % in one of 300. There the query
-  // tiles, which have one product less than the key tiles beside them, take
-  // dS's remainder as well: 0.17 %, the result's own rounding, for 3 to 5 % of
-  // the time (one head of 2,000 tokens, half the blocks kept: d 128 26.8 ->
-  // 28.1 us, d 64 24.1 -> 24.9). It would cost 7 and 13 % at one head of 9,000
-  // tokens and 11 to 14 % where the tiles fill the GPU.
-  const bool rest = p.n_tiles <= 32;
+  // bf16 shows in it: a head's dQ is off by 0.35 % of its norm, and where few
+  // rows carry that norm by up to 1.3 % (modelled on random heads of 64
+  // tokens, 0.6 % at 1,024, 0.45 % at 4,096). So in heads of up to 32 tiles of
+  // 128 rows the query tiles, which have one product less than the key tiles
+  // beside them, take dS's remainder as well: 0.17 to 0.19 %, the result's own
+  // rounding. The rule looks at the head alone, whose dQ has the same bits
+  // beside any others. It costs 3 to 5 % of the time in a call of one such head
+  // (2,000 tokens, half the blocks kept: d 128 26.8 -> 28.1 us, d 64 24.1 ->
+  // 24.9) and 9 to 17 % in one of 24 (d 128, 60 % of blocks of 64 kept: 1,000
+  // tokens 52.5 -> 61.4 us, 4,000 493 -> 559); in longer heads, whose error is
+  // the smaller one, it would cost 11 to 14 %.
+  const bool rest = p.n_qt <= 32;
 #define LOSA_BWD_CASE(D_, BLK_)                                                    \
   if (c.d == D_ && pat->block == BLK_) {                                           \
     auto run = c.out_bf16                                                          \

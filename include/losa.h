@@ -307,9 +307,11 @@ int losa_pattern_export_bwd(const losa_pattern* p, int64_t* entries, int32_t* ke
  *   an input, the workspace or another output (equal addresses are refused).
  *   bf16 q, k, v run on tensor cores: P and dS are rounded to bf16 as their
  *   operands (half a unit in the 8th bit each), as is a fp32 d_o; dQ takes
- *   dS with 16 bits in calls of at most 32 tiles of 128 rows, over which its
- *   rounding errors would not average out; all sums are fp32. fp32 q, k, v run in fp32 throughout (no tf32 rounding). No
- *   atomics: a call's results are the same bits every time.
+ *   dS with 16 bits in heads of at most 32 tiles of 128 rows, whose few rows
+ *   average its rounding errors out least; all sums are fp32. fp32 q, k, v run
+ *   in fp32 throughout (no tf32 rounding). No atomics: a call's results are
+ *   the same bits every time and, with bf16 q, k, v, a head's the same beside
+ *   any other heads.
  *   Does not allocate or synchronise, so it can be captured in a CUDA graph.
  *   Returns LOSA_ERR_ARG for a null or misaligned pointer (16 bytes; lse 4),
  *   a bad dtype, shape or scale (as losa_sparse_attn), a pattern not
