@@ -56,8 +56,11 @@ struct Eight {
 };
 
 // Three bf16 terms whose sum is x to 24 bits, as the first columns of a
-// 16-column operand row (the other columns 0).
+// 16-column operand row (the other columns 0). Finite values are kept inside
+// bf16's range; an infinity or NaN is the first term.
 __device__ __forceinline__ uint4 split3(float x) {
+  if (!isfinite(x)) return make_uint4(pack_bf16x2(x, 0.f) & 0xffffu, 0u, 0u, 0u);
+  x = fminf(fmaxf(x, -3e38f), 3e38f);
   const uint32_t h = pack_bf16x2(x, 0.f) & 0xffffu;
   const float r1 = x - __uint_as_float(h << 16);
   const uint32_t m = pack_bf16x2(r1, 0.f) & 0xffffu;
@@ -80,10 +83,11 @@ struct AugRows {
 // D cancels against the same dO that dP is made of; a bf16 one is widened.
 // Without o (fp32 path, D formed later) dO is converted only.
 // Bound: HBM. D / 8 lanes share a row, and a warp has four sets of rows in
-// flight (one row per warp at a time took 20 us at 75,776 rows of 64).
+// flight (one row per warp at a time took 20 us at 75,776 rows of 64), three CTAs
+// to an SM (two, with 86 registers a thread, cost a fifth more).
 constexpr int kDeltaSets = 4;
 template <int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 3)
     delta_kernel(const void* o, bool o_bf16, const void* d_o, bool do_bf16, int64_t rows,
                  int L, int L_pad, float* delta, void* copy, const AugRows aug) {
   constexpr int LANES = D / 8, SET = 32 / LANES;  // lanes of a row, rows of a set
@@ -92,10 +96,12 @@ __global__ void __launch_bounds__(256)
       (int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5)) * (kDeltaSets * SET) + lane / LANES;
   Eight a[kDeltaSets], b[kDeltaSets];
   bool valid[kDeltaSets];
+  float lse[kDeltaSets];
 #pragma unroll
   for (int s = 0; s < kDeltaSets; ++s) {
     const int64_t row = row0 + s * SET;
     valid[s] = row < rows && row % L_pad < L;
+    lse[s] = valid[s] && aug.q ? __ldg(aug.lse + row) : 0.f;
     if (valid[s]) {
       if (o) a[s].load(o, o_bf16, size_t(row) * D + part * 8);
       b[s].load(d_o, do_bf16, size_t(row) * D + part * 8);
@@ -129,17 +135,19 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int off = LANES / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     if (row >= rows) continue;
+    if (isnan(lse[s])) sum = NAN;  // into dQ, whichever its columns
     if (part == 0) delta[row] = sum;
     if (aug.q && part < 4) {
       // Parts 0, 1: the row's two halves of q's columns; 2, 3: of dO's. Padded
-      // rows get a score far below any other, so their weight is 0; values are
-      // kept inside bf16's range.
+      // rows get a score far below any other, so their weight is 0. A lse that
+      // is NaN becomes an infinite score: its exponential is inf or NaN in
+      // every column, that of a NaN is not (exp2_fma2's clamp drops it).
       uint4 w = make_uint4(0u, 0u, 0u, 0u);
       if (part == 0) {
-        const float t = valid[s] ? -aug.lse[row] * aug.inv_scale : -3e38f;
-        w = split3(fminf(fmaxf(t, -3e38f), 3e38f));
+        const float t = valid[s] ? -lse[s] * aug.inv_scale : -3e38f;
+        w = split3(isnan(t) ? INFINITY : t);
       } else if (part == 2) {
-        w = split3(fminf(fmaxf(-sum, -3e38f), 3e38f));
+        w = split3(-sum);
       }
       (part < 2 ? aug.q : aug.d_o)[(row >> 3) * 16 + (part & 1) * 8 + (row & 7)] = w;
     }

@@ -303,7 +303,8 @@ int losa_pattern_export_bwd(const losa_pattern* p, int64_t* entries, int32_t* ke
  *             or captured graphs that may run at the same time need one each.
  *   Rows >= L of every input are not used, whatever they hold. Values of the
  *   other rows must be finite: as in the forward call, a tile's masked pairs
- *   take weight 0, and 0 times infinity or NaN is NaN. No output may overlap
+ *   take weight 0, and 0 times infinity or NaN is NaN. A NaN in them reaches
+ *   the gradients that depend on it. No output may overlap
  *   an input, the workspace or another output (equal addresses are refused).
  *   bf16 q, k, v run on tensor cores: P and dS are rounded to bf16 as their
  *   operands (half a unit in the 8th bit each), as is a fp32 d_o; dQ takes
