@@ -499,7 +499,11 @@ __device__ __forceinline__ void fma_tile(const FmaParams& p, FmaSmem<D>& sm, int
     for (int a = 0; a < 8; ++a) {
       const int row = own0 + go + a;
       if (row >= p.L_pad) continue;
-      const float f = row >= p.L ? 0.f : use_p ? 1.f : p.scale;
+      const float f = use_p ? 1.f : p.scale;
+      if (row >= p.L) {  // 0 whatever the sums hold: 0 times NaN is not
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out[a][i] = 0.f;
+      }
 #pragma unroll
       for (int n = 0; n < 2; ++n)
         store4(dst, p.out_bf16, (base + row) * D + (gc + n * (CH / 2)) * 4, &out[a][4 * n], f);

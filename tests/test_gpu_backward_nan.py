@@ -40,3 +40,16 @@ def test_nan_reaches_the_gradients(losa, dtype, which, L, row):
         assert bad(dv[1, :L, -1][kept]).all()
     for t in (dq, dk, dv):
         assert torch.isfinite(t[0]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("which", ["q", "k", "v", "o", "lse", "do"])
+def test_padded_rows_of_the_gradients_stay_zero(losa, dtype, which):
+    L, H, d, block = 300, 2, 64, 64
+    pat = pattern_of(losa, torch.ones(H, 5, 5, dtype=torch.bool), 1, H, block)
+    q, k, v, do = torch.randn(4, 1, H, 320, d, device="cuda").to(dtype)
+    o, lse = losa.sparse_attn(q, k, v, L, pat)
+    dict(q=q, k=k, v=v, o=o, lse=lse[..., None], do=do)[which][0, 1, 290, -1] = float("nan")
+    for t in losa.sparse_attn_bwd(q, k, v, o, lse, do, L, pat):
+        assert (t[:, :, L:] == 0).all()
+    losa.check_status()
