@@ -72,7 +72,7 @@ __device__ __forceinline__ uint4 split3(float x) {
 // The bf16 path's further operand rows, which carry -lse / scale and -D into
 // its products: 8-row groups of two 8 x 16-byte core matrices each.
 struct AugRows {
-  uint4 *q, *d_o;  // null on the fp32 path
+  uint4 *q, *d_o;
   const float* lse;
   float inv_scale;
 };
@@ -86,7 +86,8 @@ struct AugRows {
 // flight (one row per warp at a time took 20 us at 75,776 rows of 64), three CTAs
 // to an SM (two, with 86 registers a thread, cost a fifth more).
 constexpr int kDeltaSets = 4;
-template <int D>
+// kAug: the bf16 path.
+template <int D, bool kAug>
 __global__ void __launch_bounds__(256, 3)
     delta_kernel(const void* o, bool o_bf16, const void* d_o, bool do_bf16, int64_t rows,
                  int L, int L_pad, float* delta, void* copy, const AugRows aug) {
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(256, 3)
   for (int s = 0; s < kDeltaSets; ++s) {
     const int64_t row = row0 + s * SET;
     valid[s] = row < rows && row % L_pad < L;
-    lse[s] = valid[s] && aug.q ? __ldg(aug.lse + row) : 0.f;
+    lse[s] = kAug && valid[s] ? __ldg(aug.lse + row) : 0.f;
     if (valid[s]) {
       if (o) a[s].load(o, o_bf16, size_t(row) * D + part * 8);
       b[s].load(d_o, do_bf16, size_t(row) * D + part * 8);
@@ -135,9 +136,9 @@ __global__ void __launch_bounds__(256, 3)
 #pragma unroll
     for (int off = LANES / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     if (row >= rows) continue;
-    if (isnan(lse[s])) sum = NAN;  // into dQ, whichever its columns
+    if (kAug && isnan(lse[s])) sum = NAN;  // into dQ, whichever its columns
     if (part == 0) delta[row] = sum;
-    if (aug.q && part < 4) {
+    if (kAug && part < 4) {
       // Parts 0, 1: the row's two halves of q's columns; 2, 3: of dO's. Padded
       // rows get a score far below any other, so their weight is 0. A lse that
       // is NaN becomes an infinite score: its exponential is inf or NaN in
@@ -590,8 +591,10 @@ cudaError_t launch_backward(const BackwardCall& c, cudaStream_t stream) {
   const int64_t per_cta = 8 * kDeltaSets * (256 / c.d);
   const unsigned grid = unsigned((rows + per_cta - 1) / per_cta);
   if (c.o || copy) {
-    (c.d == 64 ? delta_kernel<64> : delta_kernel<128>)<<<grid, 256, 0, stream>>>(
-        c.o, c.o_bf16, c.d_o, c.do_bf16, rows, c.L, L_pad, delta, copy, aug);
+    auto kernel = c.d == 64 ? (c.in_bf16 ? delta_kernel<64, true> : delta_kernel<64, false>)
+                            : (c.in_bf16 ? delta_kernel<128, true> : delta_kernel<128, false>);
+    kernel<<<grid, 256, 0, stream>>>(c.o, c.o_bf16, c.d_o, c.do_bf16, rows, c.L, L_pad, delta, copy,
+                                     aug);
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
   }
