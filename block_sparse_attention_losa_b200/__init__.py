@@ -20,6 +20,11 @@ Training and the layout around it:
 
     out, state = losa.layer_attn(xq, xk, xv, rope, pat)        # the same in one call each way
     dxq, dxk, dxv = losa.layer_attn_bwd(dout, state)
+
+rope_pack, sparse_attn, rope_unpack and layer_attn also take part in autograd:
+on tensors that require gradients they return results with a graph, whose
+backward pass makes the calls above (results written into tensors that the
+caller gives stay outside it, and so do the masses and every lse).
 """
 from __future__ import annotations
 
@@ -30,6 +35,7 @@ import os
 from typing import NamedTuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblosa.so")
@@ -338,7 +344,14 @@ def import_pattern(row_ptr, col_idx, B, H, n_blocks, block, retained_fx=None, to
 
 def sparse_attn(q, k, v, L, pattern: Pattern, scale=None, out_dtype=torch.float32, o=None,
                 lse=None, want_lse=True, stream=None):
-    """Sparse step over a frozen pattern: (o, lse or None)."""
+    """Sparse step over a frozen pattern: (o, lse or None). Where autograd
+    records it (and o and lse are not given), the backward pass is
+    sparse_attn_bwd, without o and lse for fp32 q, k, v; the pattern must be
+    prepared for it by then. lse carries no gradient."""
+    if o is None and lse is None and _tracked(q, k, v):
+        with _on(stream, q.device):
+            o, lse = _SparseAttn.apply(q, k, v, L, pattern, scale, out_dtype)
+        return o, lse if want_lse else None
     _check_qkv(q, k, v)
     B, H, Lp, d = q.shape
     if (B, H, Lp) != (pattern.B, pattern.H, pattern.n_blocks * pattern.block):
@@ -356,11 +369,48 @@ def sparse_attn(q, k, v, L, pattern: Pattern, scale=None, out_dtype=torch.float3
     return o, lse
 
 
+def _tracked(q, k, v):
+    """Whether autograd records a call on these tensors (or None)."""
+    return torch.is_grad_enabled() and (q is not None and q.requires_grad or
+                                        k is not None and k.requires_grad or
+                                        v is not None and v.requires_grad)
+
+
+def _adjacent(t):
+    """t, or a copy of it whose features are adjacent in memory."""
+    return t if t is None or t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
+
+
+def _wanted(ctx, grads):
+    """The gradients of the first inputs, those that autograd asked for."""
+    return [g if n else None for g, n in zip(grads, ctx.needs_input_grad)]
+
+
+class _SparseAttn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, L, pattern, scale, out_dtype):
+        o, lse = sparse_attn(q, k, v, L, pattern, scale=scale, out_dtype=out_dtype)
+        ctx.save_for_backward(q, k, v, o, lse)
+        ctx.call = L, pattern, scale
+        ctx.mark_non_differentiable(lse)
+        return o, lse
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, do, _):
+        q, k, v, o, lse = ctx.saved_tensors
+        if q.dtype == torch.float32:
+            o = lse = None
+        L, pattern, scale = ctx.call
+        grads = sparse_attn_bwd(q, k, v, o, lse, do.contiguous(), L, pattern, scale=scale)
+        return (*_wanted(ctx, grads), None, None, None, None)
+
+
 def _on(stream, device):
     """The context of a call's own allocations and launch: `device`, and
     `stream` if one is given, so that a workspace freed on return is reused in
     that stream's order. Nothing to enter in the usual case."""
-    if stream is None and device.index == torch.cuda.current_device():
+    if stream is None and device.index == torch._C._cuda_getDevice():
         return _HERE_AND_NOW
     stack = contextlib.ExitStack()
     stack.enter_context(torch.cuda.device(device))
@@ -538,10 +588,18 @@ def rope_pack(q, k, v, block, rope: Rope, positions=None, out_dtype=None, out=No
     of the three may be None. positions: int32 [B, L, axes] instead of the
     rope's grid and start. out: the three tensors to write."""
     x = _same("q, k, v", (q, k, v))
-    B, L, H, d = x.shape
     if block not in (32, 64, 128):
         raise ValueError("block must be 32, 64 or 128")
-    Lp = -(-L // block) * block
+    Lp = -(-x.shape[1] // block) * block
+    if out is None and _tracked(q, k, v):
+        with _on(stream, x.device):
+            return _RopePack.apply(q, k, v, Lp, rope, positions, out_dtype)
+    return _pack(x, q, k, v, Lp, rope, positions, out_dtype, out, stream)
+
+
+def _pack(x, q, k, v, Lp, rope, positions, out_dtype, out=None, stream=None):
+    """rope_pack into tensors of Lp rows; x is the first of q, k, v given."""
+    B, L, H, d = x.shape
     device, dtype = x.device, out_dtype or x.dtype
     strides = _token_strides((q, k, v))
     pos = _check_positions(positions, B, L, rope, device)
@@ -559,9 +617,10 @@ def rope_pack(q, k, v, block, rope: Rope, positions=None, out_dtype=None, out=No
                                  "inputs' device")
             dtype = y.dtype
         st = _lib.losa_rope_pack(_ptr(q), _ptr(k), _ptr(v), _dtype_code(x), strides, B, H, L, Lp,
-                                 d, rope.ref, pos, *map(_ptr, out), _dtype_code_of(dtype),
-                                 _raw_stream(stream, device))
-    _check("losa_rope_pack", st)
+                                 d, rope.ref, pos, *[t if t is None else t.data_ptr() for t in out],
+                                 _dtype_code_of(dtype), _raw_stream(stream, device))
+    if st:
+        _check("losa_rope_pack", st)
     return tuple(out)
 
 
@@ -571,6 +630,9 @@ def rope_unpack(q, k, v, L, rope: Rope, positions=None, out_dtype=None, out=None
     be None (an attention output goes back as v alone). out: the tensors to
     write, of any strides with adjacent features."""
     x = _same("q, k, v", (q, k, v))
+    if out is None and _tracked(q, k, v):
+        with _on(stream, x.device):
+            return _RopeUnpack.apply(q, k, v, int(L), rope, positions, out_dtype)
     B, H, Lp, d = x.shape
     L = int(L)
     if any(t is not None and not t.is_contiguous() for t in (q, k, v)):
@@ -595,6 +657,44 @@ def rope_unpack(q, k, v, L, rope: Rope, positions=None, out_dtype=None, out=None
     return tuple(out)
 
 
+class _RopePack(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, Lp, rope, positions, out_dtype):
+        x = _same("q, k, v", (q, k, v))
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(positions)
+        ctx.call = x.shape[1], rope, x.dtype
+        return _pack(x, q, k, v, Lp, rope, positions, out_dtype)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, *grads):
+        L, rope, dtype = ctx.call
+        grads = [None if g is None else g.contiguous() for g in _wanted(ctx, grads)]
+        if any(g is not None for g in grads):
+            grads = rope_unpack(*grads, L, rope, positions=ctx.saved_tensors[0], out_dtype=dtype)
+        return (*grads, None, None, None, None)
+
+
+class _RopeUnpack(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, L, rope, positions, out_dtype):
+        x = _same("q, k, v", (q, k, v))
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(positions)
+        ctx.call = x.shape[2], rope, x.dtype
+        return rope_unpack(q, k, v, L, rope, positions=positions, out_dtype=out_dtype)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, *grads):
+        Lp, rope, dtype = ctx.call
+        grads = [_adjacent(g) for g in _wanted(ctx, grads)]
+        if any(g is not None for g in grads):
+            grads = _pack(_same("gradients", grads), *grads, Lp, rope, ctx.saved_tensors[0], dtype)
+        return (*grads, None, None, None, None)
+
+
 class LayerState(NamedTuple):
     """What layer_attn keeps for layer_attn_bwd: packed Q, K, V and O, the row
     log-sum-exp and the call's settings."""
@@ -614,7 +714,13 @@ def layer_attn(q, k, v, rope: Rope, pattern: Pattern, positions=None, scale=None
     """A later step's attention from a layer's projections to its output
     projection's input: q, k, v [B, L, H, d] (rope_pack's) are turned and
     packed, attend over the frozen pattern, and O returns to [B, L, H, d] in
-    q's dtype. Returns (out, state); state is layer_attn_bwd's."""
+    q's dtype. Returns (out, state); state is layer_attn_bwd's, which is also
+    out's backward pass where autograd records the call."""
+    if _tracked(q, k, v):
+        keep = []
+        with _on(stream, q.device):
+            out = _LayerAttn.apply(q, k, v, rope, pattern, positions, scale, keep)
+        return out, keep[0]
     L = q.shape[1]
     with _on(stream, q.device):
         qp, kp, vp = rope_pack(q, k, v, pattern.block, rope, positions=positions, stream=stream)
@@ -639,6 +745,25 @@ def layer_attn_bwd(dout, state: LayerState, out=None, stream=None):
         grads = sparse_attn_bwd(s.q, s.k, s.v, o, lse, do, s.L, s.pattern, scale=s.scale,
                                 stream=stream)
         return rope_unpack(*grads, s.L, s.rope, positions=s.positions, out=out, stream=stream)
+
+
+class _LayerAttn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, rope, pattern, positions, scale, keep):
+        out, state = layer_attn(q, k, v, rope, pattern, positions=positions, scale=scale)
+        keep.append(state)
+        ctx.save_for_backward(*state[:5], positions)
+        ctx.call = state.L, rope, pattern, scale
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        *packed, positions = ctx.saved_tensors
+        L, rope, pattern, scale = ctx.call
+        grads = layer_attn_bwd(_adjacent(dout),
+                               LayerState(*packed, L, rope, pattern, positions, scale))
+        return (*_wanted(ctx, grads), None, None, None, None, None)
 
 
 def exp2_eval(x, stream=None):
