@@ -410,6 +410,10 @@ def _on(stream, device):
     """The context of a call's own allocations and launch: `device`, and
     `stream` if one is given, so that a workspace freed on return is reused in
     that stream's order. Nothing to enter in the usual case."""
+    if device.index is None:
+        raise ValueError("tensors must be on a CUDA device")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
     if stream is None and device.index == torch._C._cuda_getDevice():
         return _HERE_AND_NOW
     stack = contextlib.ExitStack()
