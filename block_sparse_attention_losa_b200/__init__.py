@@ -322,6 +322,8 @@ def import_pattern(row_ptr, col_idx, B, H, n_blocks, block, retained_fx=None, to
     """A Pattern from a stored host CSR (e.g. Pattern.export('cpu') of an
     earlier selection). Arrays are converted to contiguous host int32/int64."""
     device = torch.device("cuda" if device is None else device)
+    if device.type != "cuda":
+        raise ValueError("a pattern lives on a CUDA device")
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
     host = lambda t, dt: None if t is None else \

@@ -19,3 +19,8 @@ def test_host_tensors_are_refused_by_the_layer():
     x = torch.zeros(1, 24, 2, 64)
     with pytest.raises(ValueError):
         losa.layer_attn(x, x, x, rope, SimpleNamespace(block=32))
+
+
+def test_a_pattern_on_the_host_is_refused():
+    with pytest.raises(ValueError):
+        losa.import_pattern([0, 1], [0], 1, 1, 1, 32, device="cpu")
