@@ -499,7 +499,9 @@ class Rope:
             theta^(-2i/n).
     start   position of each axis's first token (a later chunk's offset).
     scale   factor on each axis's positions.
-    n_text  leading tokens that are not turned.
+    n_text  leading tokens that are not turned. Text after the video's tokens:
+            list positions per token (positions=), zeros for the text, which
+            turn nothing.
     pairing "interleaved": features (2i, 2i + 1) of an axis turn together;
             "halves": (i, i + n/2).
     """

@@ -160,7 +160,7 @@ cudaError_t launch_wait_selftest(long long limit_cycles, cudaStream_t stream) {
 
 cudaError_t launch_exp2_eval(const float* x, float* y, int64_t n, cudaStream_t stream) {
   if (n == 0) return cudaSuccess;
-  const int grid = int(std::min<int64_t>((n / 2 + 255) / 256 + 1, 148 * 8));
+  const int grid = int(std::min<int64_t>((n / 2 + 255) / 256 + 1, kSms * 8));
   exp2_eval_kernel<<<grid, 256, 0, stream>>>(x, y, n);
   return cudaGetLastError();
 }
@@ -168,7 +168,7 @@ cudaError_t launch_exp2_eval(const float* x, float* y, int64_t n, cudaStream_t s
 cudaError_t launch_f32_to_tf32(const float* src, float* dst, int64_t n, cudaStream_t stream) {
   // n is a multiple of 64 (d in {64, 128}); 16-byte aligned pointers.
   const int64_t n4 = n / 4;
-  const int grid = int(std::min<int64_t>((n4 + 255) / 256, 148 * 16));
+  const int grid = int(std::min<int64_t>((n4 + 255) / 256, kSms * 16));
   f32_to_tf32_kernel<<<grid, 256, 0, stream>>>(reinterpret_cast<const uint4*>(src),
                                                reinterpret_cast<uint4*>(dst), n4);
   return cudaGetLastError();
@@ -177,7 +177,7 @@ cudaError_t launch_f32_to_tf32(const float* src, float* dst, int64_t n, cudaStre
 cudaError_t launch_f32_to_bf16(const float* src, void* dst, int64_t n, cudaStream_t stream) {
   // n is a multiple of 64 (d in {64, 128}); 16-byte aligned pointers.
   const int64_t n4 = n / 4;
-  const int grid = int(std::min<int64_t>((n4 + 255) / 256, 148 * 16));
+  const int grid = int(std::min<int64_t>((n4 + 255) / 256, kSms * 16));
   f32_to_bf16_kernel<<<grid, 256, 0, stream>>>(reinterpret_cast<const float4*>(src),
                                                reinterpret_cast<uint2*>(dst), n4);
   return cudaGetLastError();

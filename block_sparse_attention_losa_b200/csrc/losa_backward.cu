@@ -633,7 +633,7 @@ cudaError_t launch_backward(const BackwardCall& c, cudaStream_t stream) {
   // against 103 with 128). More: two CTAs of 128 threads share an SM, and their
   // larger tiles read less shared memory (3,048 tokens, one head, d 64, 192
   // CTAs: 343 us against 404).
-  if (8 * pat->n_tiles <= 148 + 148 / 8)
+  if (8 * pat->n_tiles <= kSms + kSms / 8)
     return c.d == 64 ? run_fma<64, 256>(p, stream) : run_fma<128, 256>(p, stream);
   return c.d == 64 ? run_fma<64, 128>(p, stream) : run_fma<128, 128>(p, stream);
 }

@@ -50,6 +50,8 @@ struct NvtxRange {
   NvtxRange& operator=(const NvtxRange&) = delete;
 };
 
+constexpr int kSms = 148;  // of the B200, for which launches are sized
+
 // True when the current device is an sm_100 part (the only target built).
 bool is_sm100();
 

@@ -366,8 +366,8 @@ cudaError_t launch_rope(const RopeCall& c, cudaStream_t stream) {
   p.L_pad = c.L_pad;
   p.d = c.d;
   p.n_text = s.n_text;
-  // The grid's axes, outermost first, right-aligned to (t, h, w) so that an
-  // absent axis has extent 1 and its position is never used.
+  // The grid's axes, outermost first. Absent ones, at the end, have extent 1:
+  // place_of divides by it, and no pair refers to them.
   int ext[3] = {1, 1, 1};
   for (int a = 0; a < s.n_axes; ++a) {
     ext[a] = std::max(1, s.grid[a]);  // 0: text alone, or positions listed
@@ -395,9 +395,9 @@ cudaError_t launch_rope(const RopeCall& c, cudaStream_t stream) {
   // four heads each (CogVideoX shape, 48 heads: 118 us unsplit, 112 split),
   // and further where not even every SM would have one.
   const int64_t per_split = int64_t(nx) * c.B;
-  int64_t split = std::max<int64_t>(1, std::min<int64_t>((148 * kRopeCtas + per_split - 1) / per_split,
+  int64_t split = std::max<int64_t>(1, std::min<int64_t>((kSms * kRopeCtas + per_split - 1) / per_split,
                                                          c.H / 4));
-  if (split * per_split < 148) split = std::min<int64_t>(c.H, (148 + per_split - 1) / per_split);
+  if (split * per_split < kSms) split = std::min<int64_t>(c.H, (kSms + per_split - 1) / per_split);
   p.head_step = int((c.H + split - 1) / split);
   split = (c.H + p.head_step - 1) / p.head_step;
   const dim3 grid(nx, unsigned(split), c.B);

@@ -347,7 +347,8 @@ typedef struct {
   int start[3];    /* position of each axis's first token */
   double scale[3]; /* factor on an axis's positions (1: none) */
   double theta;    /* pair i of axis a turns by position * theta^(-2i/dim[a]) */
-  int n_text;      /* leading tokens that are not turned */
+  int n_text;      /* leading tokens that are not turned; for text elsewhere in
+                      the sequence, list positions and give it zeros */
   int pairing;     /* losa_rope_pairing */
 } losa_rope_spec;
 

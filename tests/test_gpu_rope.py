@@ -240,3 +240,19 @@ def test_binding_refusals(losa):
             call()
     with pytest.raises(TypeError):
         losa.rope_pack(x.half(), None, None, 32, rope)
+
+
+@pytest.mark.parametrize("pairing", ["interleaved", "halves"])
+def test_text_after_the_video_by_listed_positions(losa, pairing):
+    """Listed positions of zero turn nothing; the video's tokens in front turn
+    as on their grid."""
+    B, H, d, grid, dims, text = 2, 2, 64, (2, 3, 4), (16, 24, 24), 7
+    n = math.prod(grid)
+    pos = torch.zeros(B, n + text, 3, dtype=torch.int32)
+    pos[:, :n] = positions_of(grid, (0, 0, 0), 0)
+    x = torch.randn(B, n + text, H, d, device="cuda").bfloat16()
+    q = losa.rope_pack(x, None, None, 32, losa.Rope((0, 0, 0), dims, pairing=pairing),
+                       positions=pos.cuda())[0].transpose(1, 2)
+    assert torch.equal(q[:, n:n + text], x[:, n:])
+    alone = losa.rope_pack(x[:, :n], None, None, 32, losa.Rope(grid, dims, pairing=pairing))[0]
+    assert torch.equal(q[:, :n], alone.transpose(1, 2)[:, :n])
