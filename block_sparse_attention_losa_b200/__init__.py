@@ -181,7 +181,8 @@ def default_scale(d: int) -> float:
 
 def dense_mass(q, k, v, L, block, scale=None, out_dtype=torch.float32, o=None, lse=None,
                mass=None, stream=None):
-    """Construction step: (o, lse, mass) with mass [B, H, n, n], n = L_pad/block."""
+    """Construction step: (o, lse, mass) with mass [B, H, n, n], n = L_pad/block.
+    Outside autograd."""
     _check_qkv(q, k, v)
     B, H, Lp, d = q.shape
     n = Lp // block
